@@ -1,7 +1,9 @@
 /*
  * ssd.h -- libssd: the Mamba-2 SSD (state space dual) layer on AMD MI355X (gfx950): the
  * forward, its backward, the single-token recurrent step, and the block's prologue and
- * epilogue around the layer (convolution, step sizes, gate, normalisation).
+ * epilogue around the layer (convolution, step sizes, gate, normalisation); 8-bit
+ * checkpoints of activations for the backward pass; and the gated recurrence, the linear
+ * recurrence with a scalar state and a gate per channel.
  *
  * The operation ("Mamba-2: Attention's Distant Cousin", docsaid.org, sections "Writing an
  * SSM as a Matrix" and "Reducing A to a Single Number"; structured summary of arXiv
@@ -393,6 +395,156 @@ ssd_status ssd_block_fwd(const ssd_dims* dims, ssd_dtype dtype, const void* zxbc
                          const float* init_state, const float* norm_w, const float* norm_b,
                          int norm_groups, int rms, float eps, void* out, float* final_state,
                          void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- 8-bit activation checkpoints ------------------------------------------------------
+ * Activations that wait for the backward pass, held in 8 bits: every SSD_CKPT_GROUP
+ * neighbouring channels of a row share one fp32 scale.  With m = the largest |v| of the
+ * group (the last group of a row may be shorter),
+ *     scale = m / 127,  inverse = 127 / m           (each rounded to fp32 once)
+ *     code  = the integer nearest to v * inverse (the exact product; ties to even)
+ *     value = code * scale                          (rounded to the output type)
+ * with the scale at most 0x1.020406p+121, which keeps 127 * scale finite for every finite
+ * m.  A value comes back within half a step, scale / 2 up to fp32 rounding.  A group whose m
+ * is below 2^-100 (zeros among it) gets scale 0 and codes 0; a group that holds an infinity
+ * or a NaN gets scale NaN and codes 0, so all of it comes back NaN.  Codes and scales
+ * depend on the group's values alone and are the same on every run.
+ *   src, dst  rows of `width` values in `dtype`, row r at r * stride elements (stride >=
+ *             width; rows may be a column range of a wider tensor), element-aligned
+ *   codes     [rows][width] int8
+ *   scales    [rows][ceil(width / SSD_CKPT_GROUP)] fp32, 4-byte aligned */
+#define SSD_CKPT_GROUP 64
+
+/* Scales that `rows` rows of `width` values have (0 if a size is negative or too large). */
+size_t ssd_ckpt_scale_count(int64_t rows, int64_t width);
+
+/* Codes and scales of src.  rows, width >= 0, rows * src_stride < 2^60 and rows *
+ * ceil(width / 64) < 2^31 (else SSD_ERR_DIMS).  Errors otherwise as ssd_fwd. */
+ssd_status ssd_ckpt_pack(int64_t rows, int64_t width, ssd_dtype dtype, const void* src,
+                         int64_t src_stride, int8_t* codes, float* scales, void* stream);
+
+/* The values that codes and scales stand for.  Channels of dst's rows behind `width` are
+ * left as they were. */
+ssd_status ssd_ckpt_unpack(int64_t rows, int64_t width, ssd_dtype dtype, const int8_t* codes,
+                           const float* scales, void* dst, int64_t dst_stride, void* stream);
+
+/* Bytes of device workspace ssd_bwd_ckpt needs (0 if the sizes are invalid): x, B and C in
+ * `dtype` and ssd_bwd's own workspace. */
+size_t ssd_bwd_ckpt_workspace_size(const ssd_dims* dims, ssd_dtype dtype, int chunk_len);
+
+/* ssd_bwd with x, B and C kept as 8-bit checkpoints: the gradients of ssd_fwd at the values
+ * that the checkpoints stand for, rounded to `dtype`.  x is packed as [B*T] rows of H*P
+ * values, B and C as [B*T] rows of G*N.  Equal, bit for bit, to ssd_ckpt_unpack of the
+ * three followed by ssd_bwd.  Every other argument and the result are as for ssd_bwd. */
+ssd_status ssd_bwd_ckpt(const ssd_dims* dims, ssd_dtype dtype, const int8_t* x_codes,
+                        const float* x_scales, const float* dt, const float* A,
+                        const int8_t* B_codes, const float* B_scales, const int8_t* C_codes,
+                        const float* C_scales, const float* D, int chunk_len,
+                        const float* init_state, const void* dy, const float* d_final, void* dx,
+                        float* ddt, float* dA, void* dB, void* dC, float* dD, float* d_init,
+                        void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---- the gated recurrence ---------------------------------------------------------------
+ * A linear recurrence with one scalar state and one gate per channel, next to the layer's
+ * N x P state with one decay per head: for every batch element b and channel d,
+ *     q_t = 1 / (1 + exp(g_t + bias[d]))          (a_t = 1 - q_t: what the state keeps)
+ *     h_t = a_t h_{t-1} + q_t x_t = h_{t-1} + q_t (x_t - h_{t-1}),   h_{-1} = init_state
+ * computed in fp32 whatever the inputs' type; h is rounded to `dtype` once, when stored.
+ * Unlike the layer's exponentials, the gate cannot overflow: any finite g is allowed.  A
+ * non-finite x or g makes its channel non-finite from that step of that sequence on, and
+ * touches no other channel and no other sequence (in the backward pass: dx and dg of that
+ * channel in that sequence, and d_bias of that channel).
+ *
+ *   x, g       rows of D = channels values in `dtype`, row b*T + t at (b*T + t) * stride
+ *              elements (stride >= D): the two may be column ranges of one projection's rows
+ *   bias       [D] fp32, or NULL for zero
+ *   h          [B][T][D] in `dtype`
+ *   init_state, final_state, d_final, d_init    [B][D] fp32
+ *   cu_seqlens NULL, or device int32 [nseq + 1], rising from 0 to T (not checked: the
+ *              caller's contract): batch must be 1, and the row is nseq >= 1 sequences laid
+ *              end to end, each starting from zero; init_state and d_init must then be NULL
+ *              (else SSD_ERR_UNSUPPORTED), and final_state and d_final are [nseq][D] (final
+ *              state of an empty sequence: zero; its d_final is not used)
+ * x, g, h, dh, dx and dg need only the alignment of their elements, fp32 arguments and
+ * cu_seqlens 4 bytes, the workspace 16.  Sizes: B*T < 2^31, D <= 2^20, B * ceil(T/64) *
+ * ceil(D/64) < 2^31, B*T*stride < 2^60 (else SSD_ERR_DIMS); tensors may pass 2^32 elements.
+ * Results are bitwise reproducible from run to run. */
+typedef struct {
+    int64_t batch;    /* B */
+    int64_t seqlen;   /* T */
+    int64_t channels; /* D */
+} ssd_gated_dims;
+
+/* Steps between two states that the forward saves for the backward. */
+#define SSD_GATED_CHUNK 64
+
+/* What ssd_gated_fwd writes and its backward reads, in buffers of the caller.
+ *   entry_states  [B][ceil(T / SSD_GATED_CHUNK)][D] fp32: the state before each chunk's
+ *                 first step (h_{64c - 1}, or init_state)
+ *   x_codes ..    8-bit checkpoints of x and g as [B*T] rows of D values (see above): all
+ *                 four given, or all NULL */
+typedef struct {
+    float* entry_states;
+    int8_t* x_codes;
+    float* x_scales;
+    int8_t* g_codes;
+    float* g_scales;
+} ssd_gated_saved;
+
+/* Bytes of device workspace ssd_gated_fwd and ssd_gated_bwd need for these sizes, in either
+ * dtype (0 if the sizes are invalid). */
+size_t ssd_gated_workspace_size(const ssd_gated_dims* dims);
+
+/* h and (optionally) final_state; saved may be NULL (nothing is kept for a backward pass).
+ * The checkpoints hold the codes that ssd_ckpt_pack gives for x and g, bit for bit.
+ * With B = 0 or D = 0 nothing is written, with T = 0 final_state alone (init_state or zero).
+ * Errors as ssd_fwd. */
+ssd_status ssd_gated_fwd(const ssd_gated_dims* dims, ssd_dtype dtype, const void* x,
+                         int64_t x_stride, const void* g, int64_t g_stride, const float* bias,
+                         const int32_t* cu_seqlens, int64_t nseq, const float* init_state,
+                         void* h, float* final_state, const ssd_gated_saved* saved,
+                         void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of a scalar loss L through ssd_gated_fwd with the same inputs, given
+ *   dh       dL/dh, rows of D values in `dtype`, dh_stride elements apart
+ *   d_final  dL/d final_state fp32, or NULL for zero
+ *   saved    entry_states from the forward (the codes are not read)
+ * With G_t = dh_t + a_{t+1} G_{t+1} (d_final behind a sequence's last step) and h recomputed
+ * inside every chunk from its entry state,
+ *   dx_t = q_t G_t                                  (rows dx_stride elements apart, `dtype`)
+ *   dg_t = G_t (h_{t-1} - x_t) q_t a_t              (rows dg_stride elements apart, `dtype`)
+ *   d_bias = sum over batch and time of dg          ([D] fp32, or NULL to skip)
+ *   d_init = a_0 G_0                                ([B][D] fp32, or NULL to skip)
+ * d_bias is summed from the unrounded dg in a fixed order.  Every output is written in full
+ * (d_bias even with no steps; with T = 0 d_init = d_final or zero); bytes between the rows
+ * of dx and dg are left as they were.  Errors as ssd_fwd. */
+ssd_status ssd_gated_bwd(const ssd_gated_dims* dims, ssd_dtype dtype, const void* x,
+                         int64_t x_stride, const void* g, int64_t g_stride, const float* bias,
+                         const int32_t* cu_seqlens, int64_t nseq, const ssd_gated_saved* saved,
+                         const void* dh, int64_t dh_stride, const float* d_final, void* dx,
+                         int64_t dx_stride, void* dg, int64_t dg_stride, float* d_bias,
+                         float* d_init, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ssd_gated_bwd with x and g taken from the checkpoints in `saved` (all of it is required):
+ * the formulas at the values that the codes stand for, code * scale in fp32 whatever `dtype`
+ * is; the entry states are the forward's own, so an 8-bit error in the recomputed h reaches
+ * no further than its chunk. */
+ssd_status ssd_gated_bwd_ckpt(const ssd_gated_dims* dims, ssd_dtype dtype, const float* bias,
+                              const int32_t* cu_seqlens, int64_t nseq,
+                              const ssd_gated_saved* saved, const void* dh, int64_t dh_stride,
+                              const float* d_final, void* dx, int64_t dx_stride, void* dg,
+                              int64_t dg_stride, float* d_bias, float* d_init, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/* One step of the recurrence for a batch of sequences (generation): for every row b and
+ * channel d, state[b][d] <- state + q (x - state) in place and h[b][d] = state[b][d] rounded
+ * to `dtype`: the same arithmetic as one step of ssd_gated_fwd.  dims->seqlen is ignored.
+ *   x, g    rows of D values in `dtype` at x_stride, g_stride elements (>= D)
+ *   state   [B][D] fp32, read and updated in place (ssd_gated_fwd's final_state continues
+ *           here);  h [B][D] in `dtype`
+ * Alignment as above; no workspace.  Errors as ssd_fwd. */
+ssd_status ssd_gated_step(const ssd_gated_dims* dims, ssd_dtype dtype, const void* x,
+                          int64_t x_stride, const void* g, int64_t g_stride, const float* bias,
+                          float* state, void* h, void* stream);
 
 #ifdef __cplusplus
 }

@@ -6,6 +6,7 @@ HIP stream go to the C ABI.  Every step of the computation runs in libssd's kern
 there is no fallback of any kind: if libssd.so is missing the first call raises.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -19,7 +20,12 @@ EXPORTED = ("ssd_status_string", "ssd_fwd_workspace_size", "ssd_fwd", "ssd_chunk
             "ssd_chunk_scan", "ssd_decode_step", "ssd_bwd_workspace_size", "ssd_bwd",
             "ssd_block_prologue", "ssd_block_epilogue", "ssd_block_fwd_workspace_size",
             "ssd_block_fwd", "ssd_fwd_varlen_workspace_size", "ssd_fwd_varlen",
-            "ssd_bwd_saved", "ssd_fwd_noalloc", "ssd_block_fwd_norm_in_scan")
+            "ssd_bwd_saved", "ssd_fwd_noalloc", "ssd_block_fwd_norm_in_scan",
+            "ssd_ckpt_scale_count", "ssd_ckpt_pack", "ssd_ckpt_unpack",
+            "ssd_bwd_ckpt_workspace_size", "ssd_bwd_ckpt", "ssd_gated_workspace_size",
+            "ssd_gated_fwd", "ssd_gated_bwd", "ssd_gated_bwd_ckpt", "ssd_gated_step")
+CKPT_GROUP = 64    # SSD_CKPT_GROUP: neighbouring channels that share a scale
+GATED_CHUNK = 64   # SSD_GATED_CHUNK: steps between two saved states
 
 
 class SsdDims(ctypes.Structure):
@@ -29,6 +35,16 @@ class SsdDims(ctypes.Structure):
 
     def tuple(self):
         return (self.batch, self.seqlen, self.nheads, self.headdim, self.dstate, self.ngroups)
+
+
+class SsdGatedDims(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("seqlen", ctypes.c_int64),
+                ("channels", ctypes.c_int64)]
+
+
+class SsdGatedSaved(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("entry_states", "x_codes", "x_scales", "g_codes",
+                                               "g_scales")]
 
 
 class SsdError(RuntimeError):
@@ -99,6 +115,31 @@ def library(path=LIB_PATH):
     lib.ssd_fwd_varlen.restype = i
     lib.ssd_fwd_varlen.argtypes = [dims, i, vp, fp, fp, vp, vp, fp, i, vp, i64, vp, fp, vp, sz,
                                    vp]
+    lib.ssd_ckpt_scale_count.restype = sz
+    lib.ssd_ckpt_scale_count.argtypes = [i64, i64]
+    lib.ssd_ckpt_pack.restype = i
+    lib.ssd_ckpt_pack.argtypes = [i64, i64, i, vp, i64, vp, fp, vp]
+    lib.ssd_ckpt_unpack.restype = i
+    lib.ssd_ckpt_unpack.argtypes = [i64, i64, i, vp, fp, vp, i64, vp]
+    lib.ssd_bwd_ckpt_workspace_size.restype = sz
+    lib.ssd_bwd_ckpt_workspace_size.argtypes = [dims, i, i]
+    lib.ssd_bwd_ckpt.restype = i
+    lib.ssd_bwd_ckpt.argtypes = [dims, i, vp, fp, fp, fp, vp, fp, vp, fp, fp, i, fp, vp, fp, vp,
+                                 fp, fp, vp, vp, fp, fp, vp, sz, vp]
+    gdims, saved = ctypes.POINTER(SsdGatedDims), ctypes.POINTER(SsdGatedSaved)
+    lib.ssd_gated_workspace_size.restype = sz
+    lib.ssd_gated_workspace_size.argtypes = [gdims]
+    lib.ssd_gated_fwd.restype = i
+    lib.ssd_gated_fwd.argtypes = [gdims, i, vp, i64, vp, i64, fp, vp, i64, fp, vp, fp, saved, vp,
+                                  sz, vp]
+    lib.ssd_gated_bwd.restype = i
+    lib.ssd_gated_bwd.argtypes = [gdims, i, vp, i64, vp, i64, fp, vp, i64, saved, vp, i64, fp, vp,
+                                  i64, vp, i64, fp, fp, vp, sz, vp]
+    lib.ssd_gated_bwd_ckpt.restype = i
+    lib.ssd_gated_bwd_ckpt.argtypes = [gdims, i, fp, vp, i64, saved, vp, i64, fp, vp, i64, vp,
+                                       i64, fp, fp, vp, sz, vp]
+    lib.ssd_gated_step.restype = i
+    lib.ssd_gated_step.argtypes = [gdims, i, vp, i64, vp, i64, fp, fp, vp, vp]
     if path == LIB_PATH:
         _LIB = lib
     return lib
@@ -752,3 +793,367 @@ def ssd_fwd_varlen(x, dt, A, B, C, D, chunk_len, cu_seqlens, y=None, final_state
                                     _ptr(y), _ptr(final_states), _ptr(workspace),
                                     _nbytes(workspace), _stream(dev, stream)))
     return y, final_states
+
+
+# ---------------------------------------------------------------- 8-bit activation checkpoints
+def _on_stream(call):
+    """Run a binding call with its `stream` argument (when given) as torch's current stream,
+    so that outputs and workspaces allocated inside belong to the stream that uses them."""
+    @functools.wraps(call)
+    def wrapped(*args, stream=None, **kw):
+        if stream is None:
+            return call(*args, **kw)
+        with torch.cuda.stream(stream):
+            return call(*args, stream=stream, **kw)
+    return wrapped
+
+
+def _launch(fn, dev, stream, *args):
+    """fn(*args, stream) on dev's current stream with dev the current device."""
+    if dev.type != "cuda":
+        raise ValueError(f"tensors must be on a GPU, got {dev}")
+    if stream is not None and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
+    st = torch.cuda.current_stream(dev).cuda_stream
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, st))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, st))
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _rows(t, name, dtype=None, device=None):
+    """Elements between the rows of t, all its leading dimensions taken as one: the last
+    dimension contiguous, the rows evenly spaced and not overlapping (a column range of a
+    wider tensor is fine)."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    shape, width = t.shape, t.shape[-1]
+    if t.is_contiguous() or t.numel() == 0:
+        return width
+    if width > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    stride, span = width, None  # span: what the next leading dimension's stride has to be
+    for k in range(t.dim() - 2, -1, -1):
+        if shape[k] == 1:
+            continue
+        if span is None:
+            stride = t.stride(k)
+        elif t.stride(k) != span:
+            raise ValueError(f"{name}: rows must be evenly spaced")
+        span = t.stride(k) * shape[k]
+    if stride < width:
+        raise ValueError(f"{name}: rows overlap")
+    return stride
+
+
+def _code_of(t, name):
+    code = _DTYPE_CODE.get(t.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be fp32 or bf16, got {t.dtype}")
+    return code
+
+
+def ckpt_groups(width):
+    return (width + CKPT_GROUP - 1) // CKPT_GROUP
+
+
+def ssd_ckpt_scale_count(rows, width):
+    return int(library().ssd_ckpt_scale_count(int(rows), int(width)))
+
+
+def _row_count(shape):
+    n = 1
+    for v in shape[:-1]:
+        n *= v
+    return n
+
+
+@_on_stream
+def ssd_ckpt_pack(src, codes=None, scales=None, stream=None):
+    """codes, scales of src's rows (libssd.ssd_ckpt_pack).
+
+    src [..., width] fp32 or bf16 with evenly spaced rows (a column range of a wider tensor
+    is fine); codes int8 of src's shape and scales fp32 [..., ceil(width / 64)], contiguous."""
+    if src.dim() < 1:
+        raise ValueError("src must have at least one dimension")
+    dev, shape = src.device, src.shape
+    code, stride = _code_of(src, "src"), _rows(src, "src")
+    sshape = shape[:-1] + (ckpt_groups(shape[-1]),)
+    codes = torch.empty(shape, dtype=torch.int8, device=dev) if codes is None else codes
+    scales = torch.empty(sshape, dtype=torch.float32, device=dev) if scales is None else scales
+    _out(codes, "codes", torch.int8, dev, shape)
+    _out(scales, "scales", torch.float32, dev, sshape)
+    _launch(library().ssd_ckpt_pack, dev, stream, _row_count(shape), shape[-1], code, _addr(src),
+            stride, _addr(codes), _addr(scales))
+    return codes, scales
+
+
+@_on_stream
+def ssd_ckpt_unpack(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
+    """The values that codes and scales stand for (libssd.ssd_ckpt_unpack), in dtype (fp32 or
+    bf16); out may be a column range of a wider tensor."""
+    dev, shape = codes.device, codes.shape
+    if codes.dim() < 1:
+        raise ValueError("codes must have at least one dimension")
+    _need(codes, "codes", torch.int8)
+    _shape(_need(scales, "scales", torch.float32, dev), "scales",
+           shape[:-1] + (ckpt_groups(shape[-1]),))
+    out = torch.empty(shape, dtype=dtype, device=dev) if out is None else out
+    code, stride = _code_of(out, "out"), _rows(out, "out", dtype, dev)
+    _shape(out, "out", shape)
+    _launch(library().ssd_ckpt_unpack, dev, stream, _row_count(shape), shape[-1], code,
+            _addr(codes), _addr(scales), _addr(out), stride)
+    return out
+
+
+def ssd_bwd_ckpt_workspace_size(dims, dtype, chunk_len):
+    return int(library().ssd_bwd_ckpt_workspace_size(ctypes.byref(dims), _DTYPE_CODE[dtype],
+                                                     int(chunk_len)))
+
+
+@_on_stream
+def ssd_bwd_ckpt(x, dt, A, B, C, D, chunk_len, dy, ngroups, init_state=None, d_final=None,
+                 want_d_init=True, out=None, workspace=None, stream=None):
+    """ssd_bwd with x, B and C kept as 8-bit checkpoints (libssd.ssd_bwd_ckpt).
+
+    x, B, C: (codes, scales) pairs from ssd_ckpt_pack of [B,T,H*P], [B,T,G*N], [B,T,G*N]
+    rows; dy [B,T,H,P] gives the sizes and the dtype of dx, dB and dC, ngroups G.  The other
+    arguments and the returned dict are as for ssd_bwd."""
+    f32, i8, dev = torch.float32, torch.int8, dy.device
+    code = _code_of(dy, "dy")
+    _need(dy, "dy")
+    if dy.dim() != 4 or int(ngroups) < 1:
+        raise ValueError(f"dy must be [B,T,H,P] and ngroups >= 1, got {tuple(dy.shape)}, "
+                         f"{ngroups}")
+    bz, T, H, P = dy.shape
+    G = int(ngroups)
+    if B[0].dim() != 3 or B[0].shape[2] % G != 0:
+        raise ValueError(f"B's codes must be [B,T,G*N], got {tuple(B[0].shape)}")
+    N = B[0].shape[2] // G
+    for name, (codes, scales), width in (("x", x, H * P), ("B", B, G * N), ("C", C, G * N)):
+        _shape(_need(codes, f"{name}'s codes", i8, dev), f"{name}'s codes", (bz, T, width))
+        _shape(_need(scales, f"{name}'s scales", f32, dev), f"{name}'s scales",
+               (bz, T, ckpt_groups(width)))
+    for t, n, shape in ((dt, "dt", (bz, T, H)), (A, "A", (H,)), (D, "D", (H,))):
+        _shape(_need(t, n, f32, dev), n, shape)
+    fshape = (bz, H, N, P)
+    for t, n in ((init_state, "init_state"), (d_final, "d_final")):
+        if t is not None:
+            _shape(_need(t, n, f32, dev), n, fshape)
+    d = SsdDims(bz, T, H, P, N, G)
+    o = dict(out or {})
+    for k, shape, dty in (("dx", dy.shape, dy.dtype), ("ddt", dt.shape, f32), ("dA", (H,), f32),
+                          ("dB", (bz, T, G, N), dy.dtype), ("dC", (bz, T, G, N), dy.dtype),
+                          ("dD", (H,), f32)) + ((("d_init", fshape, f32),) if want_d_init else ()):
+        if o.get(k) is None:
+            o[k] = torch.empty(shape, dtype=dty, device=dev)
+        _out(o[k], k, dty, dev, shape)
+    if not want_d_init:
+        o["d_init"] = None
+    if workspace is None:
+        ws = ssd_bwd_ckpt_workspace_size(d, dy.dtype, chunk_len)
+        workspace = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
+    _need(workspace, "workspace", device=dev)
+    _launch(library().ssd_bwd_ckpt, dev, stream, ctypes.byref(d), code, _addr(x[0]), _addr(x[1]),
+            _addr(dt), _addr(A), _addr(B[0]), _addr(B[1]), _addr(C[0]), _addr(C[1]), _addr(D),
+            int(chunk_len), _addr(init_state), _addr(dy), _addr(d_final), _addr(o["dx"]),
+            _addr(o["ddt"]), _addr(o["dA"]), _addr(o["dB"]), _addr(o["dC"]), _addr(o["dD"]),
+            _addr(o["d_init"]), _addr(workspace), _nbytes(workspace))
+    return o
+
+
+# ---------------------------------------------------------------- the gated recurrence
+def ssd_gated_workspace_size(dims):
+    return int(library().ssd_gated_workspace_size(ctypes.byref(dims)))
+
+
+def _gated_dims(x, name="x"):
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [B, T, channels], got {tuple(x.shape)}")
+    return SsdGatedDims(*x.shape)
+
+
+def ssd_gated_workspace(x):
+    """A workspace for ssd_gated_fwd and its backward over rows like x [B, T, channels]."""
+    return torch.empty(max(ssd_gated_workspace_size(_gated_dims(x)), 1), dtype=torch.uint8,
+                       device=x.device)
+
+
+def ssd_gated_saved(x, ckpt=False):
+    """Buffers for what ssd_gated_fwd keeps for its backward, for rows like x [B, T, channels]:
+    entry_states, and with ckpt the 8-bit checkpoints of x and g."""
+    bz, T, D = x.shape
+    saved = dict(entry_states=torch.empty((bz, nchunks(T, GATED_CHUNK), D), dtype=torch.float32,
+                                          device=x.device))
+    if ckpt:
+        for n in ("x", "g"):
+            saved[n + "_codes"] = torch.empty((bz, T, D), dtype=torch.int8, device=x.device)
+            saved[n + "_scales"] = torch.empty((bz, T, ckpt_groups(D)), dtype=torch.float32,
+                                               device=x.device)
+    return saved
+
+
+def _gated_saved(saved, dev, shape, codes):
+    """saved's buffers checked against [B, T, channels]; codes: True (required), False (not
+    passed on) or None (passed on where given)."""
+    bz, T, D = shape
+    _shape(_need(saved.get("entry_states"), "entry_states", torch.float32, dev), "entry_states",
+           (bz, nchunks(T, GATED_CHUNK), D))
+    names = ("x_codes", "x_scales", "g_codes", "g_scales")
+    if codes is None:
+        codes = any(saved.get(n) is not None for n in names)
+    if not codes:
+        return SsdGatedSaved(_addr(saved["entry_states"]), None, None, None, None)
+    for n in names:
+        last, dty = (D, torch.int8) if n.endswith("codes") else (ckpt_groups(D), torch.float32)
+        _shape(_need(saved.get(n), n, dty, dev), n, (bz, T, last))
+    return SsdGatedSaved(_addr(saved["entry_states"]), *(_addr(saved[n]) for n in names))
+
+
+def _gated_common(dims, dev, bias, cu_seqlens, check):
+    """(number of sequences, rows of a final state) with bias and cu_seqlens checked."""
+    if bias is not None:
+        _shape(_need(bias, "bias", torch.float32, dev), "bias", (dims.channels,))
+    if cu_seqlens is None:
+        return 0, dims.batch
+    _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be [nseq + 1] with nseq >= 1")
+    if dims.batch != 1:
+        raise ValueError("a packed row has batch 1")
+    if check:
+        cu = cu_seqlens.cpu()
+        if int(cu[0]) != 0 or int(cu[-1]) != dims.seqlen or bool((cu[1:] < cu[:-1]).any()):
+            raise ValueError(f"cu_seqlens must rise from 0 to T = {dims.seqlen}")
+    return cu_seqlens.numel() - 1, cu_seqlens.numel() - 1
+
+
+def _gated_workspace(workspace, dims, dev):
+    if workspace is None:
+        workspace = torch.empty(max(ssd_gated_workspace_size(dims), 1), dtype=torch.uint8,
+                                device=dev)
+    return _need(workspace, "workspace", device=dev)
+
+
+@_on_stream
+def ssd_gated_fwd(x, g, bias=None, init_state=None, cu_seqlens=None, saved=None, h=None,
+                  final_state=None, want_final=True, workspace=None, check_cu_seqlens=True,
+                  stream=None):
+    """h, final_state of the gated recurrence (libssd.ssd_gated_fwd).
+
+    x, g [B, T, channels] fp32 or bf16, views with evenly spaced rows (column ranges of one
+    projection's output); bias [channels], init_state [B, channels] fp32 or None; saved: the
+    buffers of ssd_gated_saved(x), filled for the backward.  cu_seqlens int32 [nseq + 1] on
+    the device: a packed row (B = 1), final_state [nseq, channels]; it is copied to the host
+    and checked unless check_cu_seqlens is False (which waits for the stream)."""
+    dims, dev, f32 = _gated_dims(x), x.device, torch.float32
+    code = _code_of(x, "x")
+    xs, gs = _rows(x, "x"), _rows(g, "g", x.dtype, dev)
+    _shape(g, "g", x.shape)
+    nseq, ends = _gated_common(dims, dev, bias, cu_seqlens, check_cu_seqlens)
+    if init_state is not None:
+        _shape(_need(init_state, "init_state", f32, dev), "init_state", (x.shape[0], x.shape[2]))
+    h = torch.empty(x.shape, dtype=x.dtype, device=dev) if h is None else h
+    _out(h, "h", x.dtype, dev, x.shape)
+    fshape = (ends, x.shape[2])
+    if final_state is None and want_final:
+        final_state = torch.empty(fshape, dtype=f32, device=dev)
+    _out(final_state, "final_state", f32, dev, fshape)
+    sv = None if saved is None else ctypes.byref(_gated_saved(saved, dev, x.shape, None))
+    workspace = _gated_workspace(workspace, dims, dev)
+    _launch(library().ssd_gated_fwd, dev, stream, ctypes.byref(dims), code, _addr(x), xs,
+            _addr(g), gs, _addr(bias), _addr(cu_seqlens), nseq, _addr(init_state), _addr(h),
+            _addr(final_state), sv, _addr(workspace), _nbytes(workspace))
+    return h, final_state
+
+
+def _gated_bwd(fn, inputs, dims, shape, dtype, dev, bias, dh, saved, d_final, cu_seqlens,
+               want_d_bias, want_d_init, out, workspace, check, stream):
+    f32 = torch.float32
+    hs = _rows(dh, "dh", dtype, dev)
+    _shape(dh, "dh", shape)
+    nseq, ends = _gated_common(dims, dev, bias, cu_seqlens, check)
+    if d_final is not None:
+        _shape(_need(d_final, "d_final", f32, dev), "d_final", (ends, dims.channels))
+    sv = _gated_saved(saved, dev, shape, not inputs)
+    o = dict(out or {})
+    for k in ("dx", "dg"):
+        if o.get(k) is None:
+            o[k] = torch.empty(shape, dtype=dtype, device=dev)
+        _shape(o[k], k, shape)
+    strides = [_rows(o[k], k, dtype, dev) for k in ("dx", "dg")]
+    want_d_init = want_d_init and cu_seqlens is None
+    for k, want, kshape in (("d_bias", want_d_bias, (dims.channels,)),
+                            ("d_init", want_d_init, (dims.batch, dims.channels))):
+        if not want:
+            o[k] = None
+        elif o.get(k) is None:
+            o[k] = torch.empty(kshape, dtype=f32, device=dev)
+        _out(o[k], k, f32, dev, kshape)
+    workspace = _gated_workspace(workspace, dims, dev)
+    _launch(fn, dev, stream, ctypes.byref(dims), _DTYPE_CODE[dtype], *inputs, _addr(bias),
+            _addr(cu_seqlens), nseq, ctypes.byref(sv), _addr(dh), hs, _addr(d_final),
+            _addr(o["dx"]), strides[0], _addr(o["dg"]), strides[1], _addr(o["d_bias"]),
+            _addr(o["d_init"]), _addr(workspace), _nbytes(workspace))
+    return o
+
+
+@_on_stream
+def ssd_gated_bwd(x, g, bias, dh, saved, d_final=None, cu_seqlens=None, want_d_bias=True,
+                  want_d_init=True, out=None, workspace=None, check_cu_seqlens=True,
+                  stream=None):
+    """Gradients through ssd_gated_fwd (libssd.ssd_gated_bwd): its x, g, bias and cu_seqlens,
+    the buffers it filled (saved; entry_states alone is read) and dh, d_final.  Returns a
+    dict with dx, dg, d_bias and d_init (None where not wanted, and d_init for a packed
+    row).  out may hold preallocated tensors under those names; dx and dg may be column
+    ranges of one gradient of the projection's output."""
+    dims, dev = _gated_dims(x), x.device
+    _code_of(x, "x")
+    xs, gs = _rows(x, "x"), _rows(g, "g", x.dtype, dev)
+    _shape(g, "g", x.shape)
+    return _gated_bwd(library().ssd_gated_bwd, (_addr(x), xs, _addr(g), gs), dims, x.shape,
+                      x.dtype, dev, bias, dh, saved, d_final, cu_seqlens, want_d_bias,
+                      want_d_init, out, workspace, check_cu_seqlens, stream)
+
+
+@_on_stream
+def ssd_gated_bwd_ckpt(bias, dh, saved, d_final=None, cu_seqlens=None, want_d_bias=True,
+                       want_d_init=True, out=None, workspace=None, check_cu_seqlens=True,
+                       stream=None):
+    """ssd_gated_bwd from the 8-bit checkpoints of x and g in saved (libssd.ssd_gated_bwd_ckpt:
+    ssd_gated_saved(x, ckpt=True), filled by ssd_gated_fwd)."""
+    dims = _gated_dims(dh, "dh")
+    _code_of(dh, "dh")
+    return _gated_bwd(library().ssd_gated_bwd_ckpt, (), dims, dh.shape, dh.dtype, dh.device, bias,
+                      dh, saved, d_final, cu_seqlens, want_d_bias, want_d_init, out, workspace,
+                      check_cu_seqlens, stream)
+
+
+@_on_stream
+def ssd_gated_step(x, g, bias, state, h=None, stream=None):
+    """One step of the gated recurrence (libssd.ssd_gated_step): x, g [batch, channels] (rows
+    may be column ranges), state [batch, channels] fp32 (updated in place).  Returns h in
+    x's dtype."""
+    if x.dim() != 2:
+        raise ValueError(f"x must be [batch, channels], got {tuple(x.shape)}")
+    dev, shape = x.device, x.shape
+    code, xs, gs = _code_of(x, "x"), _rows(x, "x"), _rows(g, "g", x.dtype, dev)
+    _shape(g, "g", shape)
+    if bias is not None:
+        _shape(_need(bias, "bias", torch.float32, dev), "bias", (shape[1],))
+    _shape(_need(state, "state", torch.float32, dev), "state", shape)
+    h = torch.empty(shape, dtype=x.dtype, device=dev) if h is None else h
+    _out(h, "h", x.dtype, dev, shape)
+    dims = SsdGatedDims(shape[0], 1, shape[1])
+    _launch(library().ssd_gated_step, dev, stream, ctypes.byref(dims), code, _addr(x), xs,
+            _addr(g), gs, _addr(bias), _addr(state), _addr(h))
+    return h

@@ -1,0 +1,110 @@
+// gated.h -- the gated recurrence and the 8-bit checkpoints: arguments, launchers and the
+// element arithmetic that their kernels share.  Not part of the public ABI.
+#pragma once
+
+#include "ssd_internal.h"
+
+namespace ssd {
+
+constexpr int kGatedChunk = SSD_GATED_CHUNK;
+
+// ---- the gate --------------------------------------------------------------------------
+// q = 1 / (1 + exp(s)) and a = 1 - q = exp(s) q, each to a few fp32 ulps of ITSELF: where
+// the state keeps nearly everything q is tiny, and where it keeps nearly nothing a is, and
+// 1 - q would lose either.  exp(s) = 2^(s log2 e) by the hardware's base-2 exponential: the
+// product's rounding costs |s| 2^-24 relative, under 2e-6 for every |s| < 30.  s above 88
+// gives exp = inf and q = 0 (true value below 2^-126), s below -88 gives q = 1, a = 0;
+// NaN stays NaN in both.
+struct Gate {
+    float q, a;
+    __device__ __forceinline__ explicit Gate(float s) {
+        const float z = s * 1.4426950408889634f;
+        const float e = __builtin_amdgcn_exp2f(z);
+        q = __builtin_amdgcn_rcpf(1.f + e);
+        a = z > 126.f ? 1.f : e * q;  // inf * 0 beyond
+    }
+};
+
+// One step.  The form h + q (x - h) takes the decay as exactly 1 - q for the rounded q: with
+// a separately rounded a = 1 - q, a slow channel's decay would be off by up to 2^-25 / q of
+// its rate, the same way at every step.
+__device__ __forceinline__ float gate_step(float q, float x, float h) {
+    return fmaf(q, x - h, h);
+}
+
+// ---- 8-bit groups ----------------------------------------------------------------------
+// bits of a group's largest |v| -> its scale and inverse.  As unsigned integers NaN and
+// infinities lie above every finite value, so one integer maximum finds either.
+struct CkptScale {
+    float scale, inverse;
+    __device__ __forceinline__ explicit CkptScale(uint32_t most) {
+        const float m = __uint_as_float(most);
+        const bool tiny = most < 0x0d800000u;        // below 2^-100: 127 / m could overflow
+        const bool finite = most < 0x7f800000u;
+        // at most the largest fp32 value that 127 times stays finite
+        scale = tiny ? 0.f : finite ? fminf(m / 127.f, 0x1.0204060000000p+121f) : __uint_as_float(0x7fc00000u);
+        inverse = tiny || !finite ? 0.f : 127.f / m;
+    }
+};
+
+// The integer nearest to the exact product v * inverse, ties to even, in the low 8 bits:
+// one fused multiply-add onto 1.5 * 2^23, whose unit in the last place is 1.
+__device__ __forceinline__ uint32_t ckpt_code(float v, float inverse) {
+    return __float_as_uint(fmaf(v, inverse, 12582912.f)) & 0xffu;
+}
+
+// ---- launchers -------------------------------------------------------------------------
+struct GatedFwdArgs {
+    int B, T, D;
+    const void *x, *g;               // rows in dtype
+    long long x_stride, g_stride;
+    const float* bias;               // [D] or null
+    const int* cu;                   // packed row: [nseq + 1], or null
+    int nseq;
+    const float* init;               // [B][D] or null
+    void* h;                         // [B][T][D], dtype
+    float* final_state;              // [B or nseq][D] or null
+    float* entry;                    // [B][nC][D] or null
+    int8_t *x_codes, *g_codes;       // all four, or null
+    float *x_scales, *g_scales;
+};
+struct GatedBwdArgs {
+    int B, T, D;
+    const void *x, *g;               // rows in dtype, or null: take the codes
+    long long x_stride, g_stride;
+    const int8_t *x_codes, *g_codes;
+    const float *x_scales, *g_scales;
+    const float* bias;
+    const int* cu;
+    int nseq;
+    const float* entry;
+    const void* dh;
+    long long dh_stride;
+    const float* d_final;            // [B or nseq][D] or null
+    void *dx, *dg;
+    long long dx_stride, dg_stride;
+    float *d_bias, *d_init;          // [D], [B][D], or null
+};
+struct GatedStepArgs {
+    int B, D;
+    const void *x, *g;
+    long long x_stride, g_stride;
+    const float* bias;
+    float* state;                    // [B][D]
+    void* h;                         // [B][D], dtype
+};
+// workspace either pass needs (16-byte aligned)
+size_t gated_workspace_bytes(int B, int T, int D);
+// sizes as checked by the API; B, D >= 1
+hipError_t launch_gated_fwd(ssd_dtype dtype, const GatedFwdArgs& a, void* ws, hipStream_t st);
+hipError_t launch_gated_bwd(ssd_dtype dtype, const GatedBwdArgs& a, void* ws, hipStream_t st);
+hipError_t launch_gated_step(ssd_dtype dtype, const GatedStepArgs& a, hipStream_t st);
+
+// rows, width >= 1
+hipError_t launch_ckpt_pack(long long rows, int width, ssd_dtype dtype, const void* src,
+                            long long src_stride, int8_t* codes, float* scales, hipStream_t st);
+hipError_t launch_ckpt_unpack(long long rows, int width, ssd_dtype dtype, const int8_t* codes,
+                              const float* scales, void* dst, long long dst_stride,
+                              hipStream_t st);
+
+}  // namespace ssd

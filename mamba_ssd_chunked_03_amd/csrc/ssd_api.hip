@@ -9,7 +9,7 @@
 #include <atomic>
 #include <initializer_list>
 
-#include "ssd_internal.h"
+#include "gated.h"
 
 using ssd::Shape;
 
@@ -750,6 +750,295 @@ ssd_status ssd_fwd_varlen(const ssd_dims* dims, ssd_dtype dtype, const void* x, 
                                                         cu_seqlens, ns, final_states, st));
     return hip_status(ssd::launch_varlen_final(s, dtype, x, B, ws.dtc, ws.cs, ws.entry,
                                                cu_seqlens, ns, final_states, st));
+}
+
+}  // extern "C"
+
+// ---- 8-bit checkpoints and the gated recurrence -----------------------------------------
+
+namespace {
+// Products of sizes that index tensors with 64 bits: below 2^60 elements (8 bytes each stay
+// within the address space); counts of tiles and rows: below 2^31.
+bool below(std::initializer_list<int64_t> factors, int64_t limit) {
+    for (int64_t f : factors)
+        if (f == 0) return true;
+    int64_t acc = 1;
+    for (int64_t f : factors) {
+        if (f > (limit - 1) / acc) return false;
+        acc *= f;
+    }
+    return true;
+}
+constexpr int64_t kFar = (int64_t)1 << 60;
+
+bool misaligned_elem(std::initializer_list<const void*> ptrs, ssd_dtype dtype) {
+    for (const void* p : ptrs)
+        if (p && !aligned_elem(p, dtype)) return true;
+    return false;
+}
+
+ssd_status ckpt_check(int64_t rows, int64_t width, ssd_dtype dtype, int64_t stride) {
+    if (rows < 0 || width < 0 || stride < width || width >= kMaxElems ||
+        !below({rows, (width + SSD_CKPT_GROUP - 1) / SSD_CKPT_GROUP}, kMaxElems) ||
+        !below({rows, stride}, kFar))
+        return SSD_ERR_DIMS;
+    return valid_dtype(dtype) ? SSD_OK : SSD_ERR_UNSUPPORTED;
+}
+
+ssd_status gated_check(const ssd_gated_dims* d) {
+    if (!d) return SSD_ERR_NULL;
+    if (d->batch < 0 || d->seqlen < 0 || d->channels < 0 || d->channels > (1 << 20) ||
+        d->batch >= kMaxElems || d->seqlen >= kMaxElems)
+        return SSD_ERR_DIMS;
+    const int64_t steps = d->seqlen > 0 ? d->seqlen : 1;
+    if (!below({d->batch, steps}, kMaxElems) ||
+        !below({d->batch, (steps + 63) / 64, (d->channels + 63) / 64}, kMaxElems))
+        return SSD_ERR_DIMS;
+    return SSD_OK;
+}
+
+// x, g, dh, dx, dg: rows of D values with this stride
+bool gated_stride(const ssd_gated_dims* d, int64_t stride) {
+    return stride >= d->channels && below({d->batch, d->seqlen, stride}, kFar);
+}
+
+// packed rows: one batch element, at least one sequence, no states from outside
+ssd_status gated_packed(const ssd_gated_dims* d, const int32_t* cu, int64_t nseq,
+                        const float* state) {
+    if (!cu) return SSD_OK;
+    if (d->batch != 1 || nseq < 1 || nseq >= ((int64_t)1 << 30)) return SSD_ERR_DIMS;
+    return state ? SSD_ERR_UNSUPPORTED : SSD_OK;
+}
+
+bool saved_codes(const ssd_gated_saved* v) {
+    return v && (v->x_codes || v->x_scales || v->g_codes || v->g_scales);
+}
+bool saved_all_codes(const ssd_gated_saved* v) {
+    return v && v->x_codes && v->x_scales && v->g_codes && v->g_scales;
+}
+
+ssd_status gated_bwd_impl(const ssd_gated_dims* dims, ssd_dtype dtype, bool ckpt, const void* x,
+                          int64_t x_stride, const void* g, int64_t g_stride, const float* bias,
+                          const int32_t* cu, int64_t nseq, const ssd_gated_saved* saved,
+                          const void* dh, int64_t dh_stride, const float* d_final, void* dx,
+                          int64_t dx_stride, void* dg, int64_t dg_stride, float* d_bias,
+                          float* d_init, void* workspace, size_t workspace_bytes_given,
+                          void* stream) {
+    ssd_status r = gated_check(dims);
+    if (r != SSD_OK) return r;
+    if (!valid_dtype(dtype)) return SSD_ERR_UNSUPPORTED;
+    if ((!ckpt && (!gated_stride(dims, x_stride) || !gated_stride(dims, g_stride))) ||
+        !gated_stride(dims, dh_stride) || !gated_stride(dims, dx_stride) ||
+        !gated_stride(dims, dg_stride))
+        return SSD_ERR_DIMS;
+    r = gated_packed(dims, cu, nseq, d_init);
+    if (r != SSD_OK) return r;
+    const int B = (int)dims->batch, T = (int)dims->seqlen, D = (int)dims->channels;
+    if (B > 0 && T > 0 && D > 0) {
+        if (!saved || !saved->entry_states || !dh || !dx || !dg) return SSD_ERR_NULL;
+        if (ckpt ? !saved_all_codes(saved) : (!x || !g)) return SSD_ERR_NULL;
+    }
+    if (misaligned_elem({x, g, dh, dx, dg}, dtype) ||
+        any_misaligned4({bias, cu, d_final, d_bias, d_init}) || any_misaligned({workspace}))
+        return SSD_ERR_ALIGN;
+    if (saved && any_misaligned4({saved->entry_states, ckpt ? saved->x_scales : nullptr,
+                                  ckpt ? saved->g_scales : nullptr}))
+        return SSD_ERR_ALIGN;
+    const size_t need = ssd::gated_workspace_bytes(B, T, D);
+    if (need > 0 && (!workspace || workspace_bytes_given < need)) return SSD_ERR_WORKSPACE;
+    if (D == 0) return SSD_OK;
+    ssd::GatedBwdArgs a = {};
+    a.B = B; a.T = T; a.D = D;
+    a.x = x; a.g = g; a.x_stride = x_stride; a.g_stride = g_stride;
+    if (ckpt && saved) {
+        a.x_codes = saved->x_codes; a.g_codes = saved->g_codes;
+        a.x_scales = saved->x_scales; a.g_scales = saved->g_scales;
+    }
+    a.bias = bias;
+    a.cu = cu; a.nseq = cu ? (int)nseq : 0;
+    a.entry = saved ? saved->entry_states : nullptr;
+    a.dh = dh; a.dh_stride = dh_stride; a.d_final = d_final;
+    a.dx = dx; a.dg = dg; a.dx_stride = dx_stride; a.dg_stride = dg_stride;
+    a.d_bias = d_bias; a.d_init = d_init;
+    return hip_status(ssd::launch_gated_bwd(dtype, a, workspace, (hipStream_t)stream));
+}
+}  // namespace
+
+extern "C" {
+
+size_t ssd_ckpt_scale_count(int64_t rows, int64_t width) {
+    if (ckpt_check(rows, width, SSD_F32, width) != SSD_OK) return 0;
+    return (size_t)rows * ((width + SSD_CKPT_GROUP - 1) / SSD_CKPT_GROUP);
+}
+
+ssd_status ssd_ckpt_pack(int64_t rows, int64_t width, ssd_dtype dtype, const void* src,
+                         int64_t src_stride, int8_t* codes, float* scales, void* stream) {
+    const ssd_status r = ckpt_check(rows, width, dtype, src_stride);
+    if (r != SSD_OK) return r;
+    if (rows == 0 || width == 0) return SSD_OK;
+    if (!src || !codes || !scales) return SSD_ERR_NULL;
+    if (!aligned_elem(src, dtype) || any_misaligned4({scales})) return SSD_ERR_ALIGN;
+    return hip_status(ssd::launch_ckpt_pack(rows, (int)width, dtype, src, src_stride, codes,
+                                            scales, (hipStream_t)stream));
+}
+
+ssd_status ssd_ckpt_unpack(int64_t rows, int64_t width, ssd_dtype dtype, const int8_t* codes,
+                           const float* scales, void* dst, int64_t dst_stride, void* stream) {
+    const ssd_status r = ckpt_check(rows, width, dtype, dst_stride);
+    if (r != SSD_OK) return r;
+    if (rows == 0 || width == 0) return SSD_OK;
+    if (!codes || !scales || !dst) return SSD_ERR_NULL;
+    if (!aligned_elem(dst, dtype) || any_misaligned4({scales})) return SSD_ERR_ALIGN;
+    return hip_status(ssd::launch_ckpt_unpack(rows, (int)width, dtype, codes, scales, dst,
+                                              dst_stride, (hipStream_t)stream));
+}
+
+static size_t bwd_ckpt_bytes(const Shape& s, ssd_dtype dtype, char* base, char* part[4]) {
+    const size_t e = dtype == SSD_BF16 ? 2 : 4, bt = (size_t)s.B * s.T;
+    const size_t sizes[4] = {bt * s.H * s.P * e, bt * s.G * s.N * e, bt * s.G * s.N * e,
+                             bwd_workspace_bytes(s, nullptr, nullptr)};
+    size_t off = 0;
+    for (int i = 0; i < 4; ++i) {  // x, B, C, ssd_bwd's own
+        if (part) part[i] = base ? base + off : nullptr;
+        off += round_up(sizes[i]);
+    }
+    return off;
+}
+
+size_t ssd_bwd_ckpt_workspace_size(const ssd_dims* dims, ssd_dtype dtype, int chunk_len) {
+    Shape s;
+    if (make_shape(dims, chunk_len, &s) != SSD_OK || !valid_dtype(dtype)) return 0;
+    return bwd_ckpt_bytes(s, dtype, nullptr, nullptr);
+}
+
+ssd_status ssd_bwd_ckpt(const ssd_dims* dims, ssd_dtype dtype, const int8_t* x_codes,
+                        const float* x_scales, const float* dt, const float* A,
+                        const int8_t* B_codes, const float* B_scales, const int8_t* C_codes,
+                        const float* C_scales, const float* D, int chunk_len,
+                        const float* init_state, const void* dy, const float* d_final, void* dx,
+                        float* ddt, float* dA, void* dB, void* dC, float* dD, float* d_init,
+                        void* workspace, size_t workspace_bytes_given, void* stream) {
+    Shape s;
+    ssd_status r = make_shape(dims, chunk_len, &s);
+    if (r != SSD_OK) return r;
+    if (!valid_dtype(dtype)) return SSD_ERR_UNSUPPORTED;
+    const bool has_tokens = (size_t)s.B * s.T > 0;
+    // what ssd_bwd would refuse is refused before the first launch
+    if (!dA || !dD) return SSD_ERR_NULL;
+    if (has_tokens && (!x_codes || !x_scales || !B_codes || !B_scales || !C_codes || !C_scales ||
+                       !dt || !A || !D || !dy || !dx || !ddt || !dB || !dC))
+        return SSD_ERR_NULL;
+    if (any_misaligned({dy, dx, dB, dC, workspace}) ||
+        any_misaligned4({x_scales, B_scales, C_scales, dt, A, D, init_state, d_final, ddt, dA, dD,
+                         d_init}))
+        return SSD_ERR_ALIGN;
+    char* part[4];
+    const size_t need = bwd_ckpt_bytes(s, dtype, (char*)workspace, part);
+    if (need > 0 && (!workspace || workspace_bytes_given < need)) return SSD_ERR_WORKSPACE;
+    if (has_tokens) {
+        const long long rows = (long long)s.B * s.T;
+        const int wx = s.H * s.P, wb = s.G * s.N;
+        hipStream_t st = (hipStream_t)stream;
+        r = hip_status(
+            ssd::launch_ckpt_unpack(rows, wx, dtype, x_codes, x_scales, part[0], wx, st));
+        if (r != SSD_OK) return r;
+        r = hip_status(
+            ssd::launch_ckpt_unpack(rows, wb, dtype, B_codes, B_scales, part[1], wb, st));
+        if (r != SSD_OK) return r;
+        r = hip_status(
+            ssd::launch_ckpt_unpack(rows, wb, dtype, C_codes, C_scales, part[2], wb, st));
+        if (r != SSD_OK) return r;
+    }
+    return bwd_impl(dims, dtype, part[0], dt, A, part[1], part[2], D, chunk_len, init_state, dy,
+                    d_final, nullptr, dx, ddt, dA, dB, dC, dD, d_init, part[3],
+                    bwd_workspace_bytes(s, nullptr, nullptr), stream);
+}
+
+size_t ssd_gated_workspace_size(const ssd_gated_dims* dims) {
+    if (gated_check(dims) != SSD_OK) return 0;
+    return ssd::gated_workspace_bytes((int)dims->batch, (int)dims->seqlen, (int)dims->channels);
+}
+
+ssd_status ssd_gated_fwd(const ssd_gated_dims* dims, ssd_dtype dtype, const void* x,
+                         int64_t x_stride, const void* g, int64_t g_stride, const float* bias,
+                         const int32_t* cu_seqlens, int64_t nseq, const float* init_state,
+                         void* h, float* final_state, const ssd_gated_saved* saved,
+                         void* workspace, size_t workspace_bytes_given, void* stream) {
+    ssd_status r = gated_check(dims);
+    if (r != SSD_OK) return r;
+    if (!valid_dtype(dtype)) return SSD_ERR_UNSUPPORTED;
+    if (!gated_stride(dims, x_stride) || !gated_stride(dims, g_stride)) return SSD_ERR_DIMS;
+    r = gated_packed(dims, cu_seqlens, nseq, init_state);
+    if (r != SSD_OK) return r;
+    const int B = (int)dims->batch, T = (int)dims->seqlen, D = (int)dims->channels;
+    if (B > 0 && T > 0 && D > 0) {
+        if (!x || !g || !h || (saved && !saved->entry_states)) return SSD_ERR_NULL;
+        if (saved_codes(saved) && !saved_all_codes(saved)) return SSD_ERR_NULL;
+    }
+    if (misaligned_elem({x, g, h}, dtype) ||
+        any_misaligned4({bias, cu_seqlens, init_state, final_state}) ||
+        any_misaligned({workspace}))
+        return SSD_ERR_ALIGN;
+    if (saved && any_misaligned4({saved->entry_states, saved->x_scales, saved->g_scales}))
+        return SSD_ERR_ALIGN;
+    const size_t need = ssd::gated_workspace_bytes(B, T, D);
+    if (need > 0 && (!workspace || workspace_bytes_given < need)) return SSD_ERR_WORKSPACE;
+    if (B == 0 || D == 0) return SSD_OK;
+    ssd::GatedFwdArgs a = {};
+    a.B = B; a.T = T; a.D = D;
+    a.x = x; a.g = g; a.x_stride = x_stride; a.g_stride = g_stride;
+    a.bias = bias;
+    a.cu = cu_seqlens; a.nseq = cu_seqlens ? (int)nseq : 0;
+    a.init = init_state; a.h = h; a.final_state = final_state;
+    if (saved) {
+        a.entry = saved->entry_states;
+        a.x_codes = saved->x_codes; a.x_scales = saved->x_scales;
+        a.g_codes = saved->g_codes; a.g_scales = saved->g_scales;
+    }
+    return hip_status(ssd::launch_gated_fwd(dtype, a, workspace, (hipStream_t)stream));
+}
+
+ssd_status ssd_gated_bwd(const ssd_gated_dims* dims, ssd_dtype dtype, const void* x,
+                         int64_t x_stride, const void* g, int64_t g_stride, const float* bias,
+                         const int32_t* cu_seqlens, int64_t nseq, const ssd_gated_saved* saved,
+                         const void* dh, int64_t dh_stride, const float* d_final, void* dx,
+                         int64_t dx_stride, void* dg, int64_t dg_stride, float* d_bias,
+                         float* d_init, void* workspace, size_t workspace_bytes_given,
+                         void* stream) {
+    return gated_bwd_impl(dims, dtype, false, x, x_stride, g, g_stride, bias, cu_seqlens, nseq,
+                          saved, dh, dh_stride, d_final, dx, dx_stride, dg, dg_stride, d_bias,
+                          d_init, workspace, workspace_bytes_given, stream);
+}
+
+ssd_status ssd_gated_bwd_ckpt(const ssd_gated_dims* dims, ssd_dtype dtype, const float* bias,
+                              const int32_t* cu_seqlens, int64_t nseq,
+                              const ssd_gated_saved* saved, const void* dh, int64_t dh_stride,
+                              const float* d_final, void* dx, int64_t dx_stride, void* dg,
+                              int64_t dg_stride, float* d_bias, float* d_init, void* workspace,
+                              size_t workspace_bytes_given, void* stream) {
+    return gated_bwd_impl(dims, dtype, true, nullptr, 0, nullptr, 0, bias, cu_seqlens, nseq,
+                          saved, dh, dh_stride, d_final, dx, dx_stride, dg, dg_stride, d_bias,
+                          d_init, workspace, workspace_bytes_given, stream);
+}
+
+ssd_status ssd_gated_step(const ssd_gated_dims* dims, ssd_dtype dtype, const void* x,
+                          int64_t x_stride, const void* g, int64_t g_stride, const float* bias,
+                          float* state, void* h, void* stream) {
+    if (!dims) return SSD_ERR_NULL;
+    ssd_gated_dims one = *dims;
+    one.seqlen = 1;
+    const ssd_status r = gated_check(&one);
+    if (r != SSD_OK) return r;
+    if (!valid_dtype(dtype)) return SSD_ERR_UNSUPPORTED;
+    if (!gated_stride(&one, x_stride) || !gated_stride(&one, g_stride)) return SSD_ERR_DIMS;
+    if (one.batch == 0 || one.channels == 0) return SSD_OK;
+    if (!x || !g || !state || !h) return SSD_ERR_NULL;
+    if (misaligned_elem({x, g, h}, dtype) || any_misaligned4({bias, state})) return SSD_ERR_ALIGN;
+    ssd::GatedStepArgs a;
+    a.B = (int)one.batch; a.D = (int)one.channels;
+    a.x = x; a.g = g; a.x_stride = x_stride; a.g_stride = g_stride;
+    a.bias = bias; a.state = state; a.h = h;
+    return hip_status(ssd::launch_gated_step(dtype, a, (hipStream_t)stream));
 }
 
 }  // extern "C"

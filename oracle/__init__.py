@@ -12,6 +12,7 @@ Contents
   chunk_states     per-chunk states that start from zero (the chunk's own input only)
   entry_states     the state entering every chunk (init for chunk 0)
   chunk_entry_grads  dL/d(entry state of a chunk) through that chunk's own outputs only
+  gated            the gated recurrence, its gradient and the 8-bit checkpoints (numpy)
 
 Sources: "Mamba-2: Attention's Distant Cousin" (docsaid.org), sections "Writing an SSM
 as a Matrix", "Reducing A to a Single Number", "Working Through Four Tokens"; and the
@@ -25,6 +26,7 @@ import numpy as np
 
 from . import build as _build
 from .quadratic import ssd_quadratic, one_ss_mask  # noqa: F401
+from . import gated  # noqa: F401
 
 _LIB = None
 
