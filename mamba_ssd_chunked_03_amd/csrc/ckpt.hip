@@ -1,7 +1,10 @@
 // ckpt.hip -- activations held in 8 bits: pack and unpack.
 //
 // Every 64 neighbouring channels of a row share a scale (m / 127, m the largest |v|); a
-// code is the integer nearest to v * (127 / m).  One thread per group.
+// code is the integer nearest to v * (127 / m).  Bound by HBM: pack reads 2 or 4 bytes a
+// value and writes 1 + 1/16, unpack the reverse.  A lane holds one 16-byte piece of a row (8
+// bf16 or 4 fp32), so a group is 8 or 16 neighbouring lanes and its maximum a few DPP steps
+// inside them; a thread has kRows rows in flight.
 #include "gated.h"
 
 namespace ssd {
@@ -9,70 +12,192 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kGroup = SSD_CKPT_GROUP;
+constexpr int kRows = 4;
+
+// Pieces of a row are a power of two of neighbouring threads (at most a whole workgroup):
+// block -> (rows, columns), thread -> (row, piece).
+struct Grid {
+    long long rows;
+    int width, groups;
+    int shift;        // log2 of the threads along a row
+    unsigned cols;    // workgroups along a row
+};
+
+template <typename T> constexpr int kVec = 16 / sizeof(T);
+
+template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+// the maximum over the LANES (8 or 16) neighbouring lanes of a group, in all of them
+template <int LANES> __device__ __forceinline__ uint32_t group_max(uint32_t v) {
+    v = max(v, dpp<0xb1>(v));               // quad_perm [1,0,3,2]
+    v = max(v, dpp<0x4e>(v));               // quad_perm [2,3,0,1]
+    v = max(v, dpp<0x141>(v));              // row_half_mirror: the other quad of 8
+    if (LANES == 16) v = max(v, dpp<0x140>(v));  // row_mirror: the other 8 of 16
+    return v;
+}
+
+struct __attribute__((packed, aligned(1))) Any16 { uint32_t w[4]; };
+struct __attribute__((packed, aligned(1))) Any8 { uint32_t w[2]; };
+struct __attribute__((packed, aligned(1))) Any4 { uint32_t w[1]; };
+template <int BYTES> struct AnyOf;
+template <> struct AnyOf<16> { using type = Any16; };
+template <> struct AnyOf<8> { using type = Any8; };
+template <> struct AnyOf<4> { using type = Any4; };
+
+// rows need only element alignment: pieces are unaligned 16-byte accesses
+template <typename T>
+__device__ __forceinline__ void load_piece(float (&v)[kVec<T>], const T* p, int n) {
+    constexpr int V = kVec<T>;
+    if (n >= V) {
+        const Any16 b = *(const Any16*)p;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            v[i] = sizeof(T) == 4 ? __uint_as_float(b.w[i % 4])
+                                  : __uint_as_float(i & 1 ? b.w[i / 2] & 0xffff0000u
+                                                          : b.w[i / 2] << 16);
+    } else {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = i < n ? to_f32(p[i]) : 0.f;
+    }
+}
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ckpt_pack_kernel(const T* src, long long stride,
-                                                             long long groups, int per_row,
-                                                             int width, int8_t* codes,
+                                                             Grid g, int8_t* codes,
                                                              float* scales) {
-    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (id >= groups) return;
-    const long long row = id / per_row;
-    const int c0 = (int)(id % per_row) * kGroup, n = min(kGroup, width - c0);
-    const T* v = src + row * stride + c0;
-    uint32_t most = 0;
-    for (int i = 0; i < n; ++i)
-        most = max(most, __float_as_uint(to_f32(v[i])) & 0x7fffffffu);
-    const CkptScale s(most);
-    scales[id] = s.scale;
-    for (int i = 0; i < n; ++i)
-        codes[row * width + c0 + i] =
-            most < 0x7f800000u ? (int8_t)ckpt_code(to_f32(v[i]), s.inverse) : 0;
+    constexpr int V = kVec<T>, L = kGroup / V;
+    const int per = kThreads >> g.shift;  // rows of a workgroup at a time
+    const unsigned rb = blockIdx.x / g.cols, cb = blockIdx.x % g.cols;
+    const int c0 = ((int)(cb << g.shift) + (threadIdx.x & ((1 << g.shift) - 1))) * V;
+    const int n = g.width - c0;
+    const long long row0 = (long long)rb * per * kRows + (threadIdx.x >> g.shift);
+    float v[kRows][V];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const long long row = row0 + u * per;
+        load_piece<T>(v[u], src + row * stride + c0, row < g.rows ? n : 0);
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const long long row = row0 + u * per;
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) most = max(most, __float_as_uint(v[u][i]) & 0x7fffffffu);
+        most = group_max<L>(most);  // every lane of the wave takes part
+        const CkptScale s(most);
+        if (row >= g.rows || n <= 0) continue;
+        if (c0 % kGroup == 0) scales[row * g.groups + c0 / kGroup] = s.scale;
+        uint32_t w[V / 4];
+#pragma unroll
+        for (int k = 0; k < V / 4; ++k) w[k] = ckpt_codes(&v[u][4 * k], s);
+        int8_t* p = codes + row * g.width + c0;
+        if (n >= V) {
+            typename AnyOf<V>::type b;
+#pragma unroll
+            for (int k = 0; k < V / 4; ++k) b.w[k] = w[k];
+            *(typename AnyOf<V>::type*)p = b;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < n) p[i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
+        }
+    }
 }
 
 template <typename T>
 __global__ __launch_bounds__(kThreads) void ckpt_unpack_kernel(const int8_t* codes,
-                                                               const float* scales,
-                                                               long long groups, int per_row,
-                                                               int width, T* dst,
-                                                               long long stride) {
-    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (id >= groups) return;
-    const long long row = id / per_row;
-    const int c0 = (int)(id % per_row) * kGroup, n = min(kGroup, width - c0);
-    const float s = scales[id];
-    for (int i = 0; i < n; ++i)
-        dst[row * stride + c0 + i] = from_f32<T>((float)codes[row * width + c0 + i] * s);
+                                                               const float* scales, Grid g,
+                                                               T* dst, long long stride) {
+    constexpr int V = kVec<T>;
+    const int per = kThreads >> g.shift;
+    const unsigned rb = blockIdx.x / g.cols, cb = blockIdx.x % g.cols;
+    const int c0 = ((int)(cb << g.shift) + (threadIdx.x & ((1 << g.shift) - 1))) * V;
+    const int n = g.width - c0;
+    if (n <= 0) return;
+    const long long row0 = (long long)rb * per * kRows + (threadIdx.x >> g.shift);
+    typename AnyOf<V>::type b[kRows];
+    float s[kRows];
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const long long row = row0 + u * per;
+        if (row >= g.rows) continue;
+        const int8_t* p = codes + row * g.width + c0;
+        s[u] = scales[row * g.groups + c0 / kGroup];
+        if (n >= V) {
+            b[u] = *(const typename AnyOf<V>::type*)p;
+        } else {
+#pragma unroll
+            for (int k = 0; k < V / 4; ++k) b[u].w[k] = 0;
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < n) b[u].w[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kRows; ++u) {
+        const long long row = row0 + u * per;
+        if (row >= g.rows) continue;
+        T* p = dst + row * stride + c0;
+        union { T t[V]; Any16 a; } o;
+#pragma unroll
+        for (int i = 0; i < V; ++i)
+            o.t[i] = from_f32<T>((float)(int8_t)(b[u].w[i / 4] >> (8 * (i % 4))) * s[u]);
+        if (n >= V) {
+            *(Any16*)p = o.a;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i < n) p[i] = o.t[i];
+        }
+    }
+}
+
+template <typename T> Grid grid_of(long long rows, int width, unsigned* blocks) {
+    Grid g;
+    g.rows = rows;
+    g.width = width;
+    g.groups = (width + kGroup - 1) / kGroup;
+    const int lanes = kGroup / kVec<T>;  // a group's lanes stay together
+    g.shift = lanes == 8 ? 3 : 4;
+    while ((1 << g.shift) < kThreads && ((long long)kVec<T> << g.shift) < width) ++g.shift;
+    g.cols = (unsigned)((width + ((long long)kVec<T> << g.shift) - 1) /
+                        ((long long)kVec<T> << g.shift));
+    const long long per = (long long)(kThreads >> g.shift) * kRows;
+    *blocks = (unsigned)((rows + per - 1) / per * g.cols);
+    return g;
 }
 
 }  // namespace
 
 hipError_t launch_ckpt_pack(long long rows, int width, ssd_dtype dtype, const void* src,
                             long long src_stride, int8_t* codes, float* scales, hipStream_t st) {
-    const int per_row = (width + kGroup - 1) / kGroup;
-    const long long groups = rows * per_row;
-    const unsigned blocks = (unsigned)((groups + kThreads - 1) / kThreads);
-    if (dtype == SSD_F32)
-        ckpt_pack_kernel<float><<<blocks, kThreads, 0, st>>>(
-            (const float*)src, src_stride, groups, per_row, width, codes, scales);
-    else
-        ckpt_pack_kernel<__bf16><<<blocks, kThreads, 0, st>>>(
-            (const __bf16*)src, src_stride, groups, per_row, width, codes, scales);
+    unsigned blocks;
+    if (dtype == SSD_F32) {
+        const Grid g = grid_of<float>(rows, width, &blocks);
+        ckpt_pack_kernel<float>
+            <<<blocks, kThreads, 0, st>>>((const float*)src, src_stride, g, codes, scales);
+    } else {
+        const Grid g = grid_of<__bf16>(rows, width, &blocks);
+        ckpt_pack_kernel<__bf16>
+            <<<blocks, kThreads, 0, st>>>((const __bf16*)src, src_stride, g, codes, scales);
+    }
     return hipGetLastError();
 }
 
 hipError_t launch_ckpt_unpack(long long rows, int width, ssd_dtype dtype, const int8_t* codes,
                               const float* scales, void* dst, long long dst_stride,
                               hipStream_t st) {
-    const int per_row = (width + kGroup - 1) / kGroup;
-    const long long groups = rows * per_row;
-    const unsigned blocks = (unsigned)((groups + kThreads - 1) / kThreads);
-    if (dtype == SSD_F32)
-        ckpt_unpack_kernel<float><<<blocks, kThreads, 0, st>>>(
-            codes, scales, groups, per_row, width, (float*)dst, dst_stride);
-    else
-        ckpt_unpack_kernel<__bf16><<<blocks, kThreads, 0, st>>>(
-            codes, scales, groups, per_row, width, (__bf16*)dst, dst_stride);
+    unsigned blocks;
+    if (dtype == SSD_F32) {
+        const Grid g = grid_of<float>(rows, width, &blocks);
+        ckpt_unpack_kernel<float>
+            <<<blocks, kThreads, 0, st>>>(codes, scales, g, (float*)dst, dst_stride);
+    } else {
+        const Grid g = grid_of<__bf16>(rows, width, &blocks);
+        ckpt_unpack_kernel<__bf16>
+            <<<blocks, kThreads, 0, st>>>(codes, scales, g, (__bf16*)dst, dst_stride);
+    }
     return hipGetLastError();
 }
 

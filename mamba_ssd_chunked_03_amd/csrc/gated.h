@@ -9,16 +9,19 @@ namespace ssd {
 constexpr int kGatedChunk = SSD_GATED_CHUNK;
 
 // ---- the gate --------------------------------------------------------------------------
-// q = 1 / (1 + exp(s)) and a = 1 - q = exp(s) q, each to a few fp32 ulps of ITSELF: where
-// the state keeps nearly everything q is tiny, and where it keeps nearly nothing a is, and
-// 1 - q would lose either.  exp(s) = 2^(s log2 e) by the hardware's base-2 exponential: the
-// product's rounding costs |s| 2^-24 relative, under 2e-6 for every |s| < 30.  s above 88
-// gives exp = inf and q = 0 (true value below 2^-126), s below -88 gives q = 1, a = 0;
+// With z = (g + bias) log2 e, formed as fma(g, log2 e, bias log2 e): q = 1 / (1 + 2^z) and
+// a = 1 - q = 2^z q, each to a few fp32 ulps of ITSELF: where the state keeps nearly
+// everything q is tiny, and where it keeps nearly nothing a is, and 1 - q would lose either.
+// The roundings of z cost |z| 2^-24 relative, under 3e-6 for every |g + bias| < 30.  z above
+// 128 gives 2^z = inf and q = 0 (true value below 2^-127), z below -126 gives q = 1, a = 0;
 // NaN stays NaN in both.
+constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float gate_q(float z) {
+    return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(z));
+}
 struct Gate {
     float q, a;
-    __device__ __forceinline__ explicit Gate(float s) {
-        const float z = s * 1.4426950408889634f;
+    __device__ __forceinline__ explicit Gate(float z) {
         const float e = __builtin_amdgcn_exp2f(z);
         q = __builtin_amdgcn_rcpf(1.f + e);
         a = z > 126.f ? 1.f : e * q;  // inf * 0 beyond
@@ -47,10 +50,17 @@ struct CkptScale {
     }
 };
 
-// The integer nearest to the exact product v * inverse, ties to even, in the low 8 bits:
-// one fused multiply-add onto 1.5 * 2^23, whose unit in the last place is 1.
-__device__ __forceinline__ uint32_t ckpt_code(float v, float inverse) {
-    return __float_as_uint(fmaf(v, inverse, 12582912.f)) & 0xffu;
+// The codes of four neighbouring channels: the integers nearest to the exact products
+// v * inverse, ties to even, in the low 8 bits of one fused multiply-add each onto 1.5 * 2^23,
+// whose unit in the last place is 1.  A group that is not finite has inverse 0, and its codes
+// are 0 whatever v is.
+__device__ __forceinline__ uint32_t ckpt_codes(const float* v, const CkptScale& s) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __float_as_uint(fmaf(v[i], s.inverse, 12582912.f));
+    const uint32_t lo = __builtin_amdgcn_perm(w[1], w[0], 0x0c0c0400u);
+    const uint32_t hi = __builtin_amdgcn_perm(w[3], w[2], 0x04000c0cu);
+    return s.inverse == 0.f ? 0u : lo | hi;
 }
 
 // ---- launchers -------------------------------------------------------------------------
