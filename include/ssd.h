@@ -466,7 +466,8 @@ ssd_status ssd_bwd_ckpt(const ssd_dims* dims, ssd_dtype dtype, const int8_t* x_c
  *              state of an empty sequence: zero; its d_final is not used)
  * x, g, h, dh, dx and dg need only the alignment of their elements, fp32 arguments and
  * cu_seqlens 4 bytes, the workspace 16.  Sizes: B*T < 2^31, D <= 2^20, B * ceil(T/64) *
- * ceil(D/64) < 2^31, B*T*stride < 2^60 (else SSD_ERR_DIMS); tensors may pass 2^32 elements.
+ * ceil(D/64) < 2^31, B*T*stride < 2^60, and min(T, 256) * stride < 2^29 for T > 1 (else
+ * SSD_ERR_DIMS); tensors may pass 2^32 elements.
  * Results are bitwise reproducible from run to run. */
 typedef struct {
     int64_t batch;    /* B */

@@ -25,25 +25,7 @@ struct Grid {
 
 template <typename T> constexpr int kVec = 16 / sizeof(T);
 
-template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
-}
-// the maximum over the LANES (8 or 16) neighbouring lanes of a group, in all of them
-template <int LANES> __device__ __forceinline__ uint32_t group_max(uint32_t v) {
-    v = max(v, dpp<0xb1>(v));               // quad_perm [1,0,3,2]
-    v = max(v, dpp<0x4e>(v));               // quad_perm [2,3,0,1]
-    v = max(v, dpp<0x141>(v));              // row_half_mirror: the other quad of 8
-    if (LANES == 16) v = max(v, dpp<0x140>(v));  // row_mirror: the other 8 of 16
-    return v;
-}
-
 struct __attribute__((packed, aligned(1))) Any16 { uint32_t w[4]; };
-struct __attribute__((packed, aligned(1))) Any8 { uint32_t w[2]; };
-struct __attribute__((packed, aligned(1))) Any4 { uint32_t w[1]; };
-template <int BYTES> struct AnyOf;
-template <> struct AnyOf<16> { using type = Any16; };
-template <> struct AnyOf<8> { using type = Any8; };
-template <> struct AnyOf<4> { using type = Any4; };
 
 // rows need only element alignment: pieces are unaligned 16-byte accesses
 template <typename T>
@@ -84,24 +66,11 @@ __global__ __launch_bounds__(kThreads) void ckpt_pack_kernel(const T* src, long 
         uint32_t most = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) most = max(most, __float_as_uint(v[u][i]) & 0x7fffffffu);
-        most = group_max<L>(most);  // every lane of the wave takes part
+        most = ckpt_group_max<L>(most);  // every lane of the wave takes part
         const CkptScale s(most);
         if (row >= g.rows || n <= 0) continue;
         if (c0 % kGroup == 0) scales[row * g.groups + c0 / kGroup] = s.scale;
-        uint32_t w[V / 4];
-#pragma unroll
-        for (int k = 0; k < V / 4; ++k) w[k] = ckpt_codes(&v[u][4 * k], s);
-        int8_t* p = codes + row * g.width + c0;
-        if (n >= V) {
-            typename AnyOf<V>::type b;
-#pragma unroll
-            for (int k = 0; k < V / 4; ++k) b.w[k] = w[k];
-            *(typename AnyOf<V>::type*)p = b;
-        } else {
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i < n) p[i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
-        }
+        ckpt_store<V>(codes + row * g.width + c0, v[u], s, 0, min(n, V));
     }
 }
 
@@ -116,7 +85,7 @@ __global__ __launch_bounds__(kThreads) void ckpt_unpack_kernel(const int8_t* cod
     const int n = g.width - c0;
     if (n <= 0) return;
     const long long row0 = (long long)rb * per * kRows + (threadIdx.x >> g.shift);
-    typename AnyOf<V>::type b[kRows];
+    CkptPiece<V> b[kRows];
     float s[kRows];
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
@@ -124,15 +93,8 @@ __global__ __launch_bounds__(kThreads) void ckpt_unpack_kernel(const int8_t* cod
         if (row >= g.rows) continue;
         const int8_t* p = codes + row * g.width + c0;
         s[u] = scales[row * g.groups + c0 / kGroup];
-        if (n >= V) {
-            b[u] = *(const typename AnyOf<V>::type*)p;
-        } else {
-#pragma unroll
-            for (int k = 0; k < V / 4; ++k) b[u].w[k] = 0;
-#pragma unroll
-            for (int i = 0; i < V; ++i)
-                if (i < n) b[u].w[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
-        }
+        if (n >= V) b[u].load(p);
+        else b[u].load_part(p, n);
     }
 #pragma unroll
     for (int u = 0; u < kRows; ++u) {
@@ -142,7 +104,7 @@ __global__ __launch_bounds__(kThreads) void ckpt_unpack_kernel(const int8_t* cod
         union { T t[V]; Any16 a; } o;
 #pragma unroll
         for (int i = 0; i < V; ++i)
-            o.t[i] = from_f32<T>((float)(int8_t)(b[u].w[i / 4] >> (8 * (i % 4))) * s[u]);
+            o.t[i] = from_f32<T>(b[u].get(i) * s[u]);
         if (n >= V) {
             *(Any16*)p = o.a;
         } else {

@@ -63,6 +63,68 @@ __device__ __forceinline__ uint32_t ckpt_codes(const float* v, const CkptScale& 
     return s.inverse == 0.f ? 0u : lo | hi;
 }
 
+// The maximum over the LANES (8 or 16) neighbouring lanes of a group, in all of them.
+template <int CTRL> __device__ __forceinline__ uint32_t dpp_move(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true);
+}
+template <int LANES> __device__ __forceinline__ uint32_t ckpt_group_max(uint32_t v) {
+    v = max(v, dpp_move<0xb1>(v));                    // quad_perm [1,0,3,2]
+    v = max(v, dpp_move<0x4e>(v));                    // quad_perm [2,3,0,1]
+    v = max(v, dpp_move<0x141>(v));                   // row_half_mirror: the other quad of 8
+    if (LANES == 16) v = max(v, dpp_move<0x140>(v));  // row_mirror: the other 8 of 16
+    return v;
+}
+
+// V codes of neighbouring channels (4 or 8 bytes at any alignment).
+template <int V> struct CkptPiece {
+    struct __attribute__((packed, aligned(1))) Any { uint32_t w[V / 4]; };
+    uint32_t w[V / 4];
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < V / 4; ++k) w[k] = 0;
+    }
+    __device__ __forceinline__ void load(const int8_t* p) {
+        const Any b = *(const Any*)p;
+#pragma unroll
+        for (int k = 0; k < V / 4; ++k) w[k] = b.w[k];
+    }
+    // the first n < V, zeros behind them
+    __device__ __forceinline__ void load_part(const int8_t* p, int n) {
+        clear();
+#pragma unroll
+        for (int i = 0; i < V - 1; ++i)
+            if (i < n) w[i / 4] |= (uint32_t)(uint8_t)p[i] << (8 * (i % 4));
+    }
+    // elements lo to hi
+    __device__ __forceinline__ void store(int8_t* p, int lo, int hi) const {
+        if (hi - lo == V) {
+            Any b;
+#pragma unroll
+            for (int k = 0; k < V / 4; ++k) b.w[k] = w[k];
+            *(Any*)p = b;
+        } else {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (i >= lo && i < hi) p[i] = (int8_t)(w[i / 4] >> (8 * (i % 4)));
+        }
+    }
+    __device__ __forceinline__ float get(int i) const {
+        return (float)(int8_t)(w[i / 4] >> (8 * (i % 4)));
+    }
+    __device__ __forceinline__ void renew() {
+#pragma unroll
+        for (int k = 0; k < V / 4; ++k) asm volatile("" : "+v"(w[k]));
+    }
+};
+template <int V>
+__device__ __forceinline__ void ckpt_store(int8_t* p, const float (&v)[V], const CkptScale& s,
+                                           int lo, int hi) {
+    CkptPiece<V> c;
+#pragma unroll
+    for (int k = 0; k < V / 4; ++k) c.w[k] = ckpt_codes(&v[4 * k], s);
+    c.store(p, lo, hi);
+}
+
 // ---- launchers -------------------------------------------------------------------------
 struct GatedFwdArgs {
     int B, T, D;

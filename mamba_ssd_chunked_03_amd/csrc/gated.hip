@@ -6,13 +6,13 @@
 //
 // Both recursions are affine in what they carry: over a span of steps the carry v becomes
 // H + P v, with P the product of the span's a and H its result from zero, and two spans
-// combine to (P2 P1, H2 + P2 H1).  A workgroup owns a tile of 64 channels and 32 runs of S
-// steps; one pass over HBM:
-//   1. every thread loads its run (S steps of 4 neighbouring channels) into registers and
-//      forms the run's (P, H);
-//   2. one wave, a lane per channel, scans the 32 runs through LDS into prefixes and the
+// combine to (P2 P1, H2 + P2 H1).  A workgroup owns a tile of 256 bytes of channels and 32
+// runs of S steps; one pass over HBM:
+//   1. every thread loads its run (S steps of the neighbouring channels that 16 bytes hold)
+//      into registers and forms the run's (P, H);
+//   2. a lane per channel scans the 32 runs through LDS into prefixes and the
 //      tile's own (P, H), and finds the carry into the tile: the tiles of one chain (batch
-//      element and 64 channels) publish their (P, H), every 16th also the carry out of it,
+//      element and channels) publish their (P, H), every 16th also the carry out of it,
 //      and a tile combines the last such carry with the spans behind it;
 //   3. every thread takes its run's carry and goes through the run again, from registers.
 // The backward does this for h from the saved entry states (no waiting) and, last step
@@ -24,605 +24,841 @@
 // waits itself, and the carry out of a 16th tile waits for earlier tiles only.  A published
 // word holds the value and a tag in one 64-bit atomic store, so a reader that sees the tag
 // has the value, whatever the order of other stores.
+#include <initializer_list>
+
 #include "gated.h"
 
 namespace ssd {
 namespace {
 
-constexpr int kTileThreads = 512;
-constexpr int kRuns = 32;      // runs of a tile; 16 lanes of 4 channels each
-constexpr int kCols = 64;      // channels of a tile
-// Steps of a run, so that what a thread holds of it (raw x and g, the backward's dh too) is
-// 32 to 64 registers: more would halve the waves in flight.
-constexpr int kFwdSteps = 8;
-constexpr int bwd_steps(ssd_dtype t) { return t == SSD_F32 ? 4 : 8; }
+constexpr int kLanes = 16;     // lanes along a row of a tile
+#ifndef X_FR
+#define X_FR 32
+#endif
+#ifndef X_BR
+#define X_BR 32
+#endif
+constexpr int kFwdRuns = X_FR, kBwdRuns = X_BR;      // runs of a tile
+#ifndef X_LOOK
+#define X_LOOK 8
+#endif
+constexpr int kLook = X_LOOK;       // spans looked at together
+#ifndef X_SCAN
+#define X_SCAN 8
+#endif
+constexpr int kScan = X_SCAN;       // runs scanned together
+#ifndef X_FV
+#define X_FV 8
+#define X_FS 4
+#endif
+#ifndef X_BV
+#define X_BV 4
+#define X_BS 4
+#endif
+constexpr int fwd_vec(ssd_dtype t) { return t == SSD_F32 ? 4 : X_FV; }
+constexpr int bwd_vec(ssd_dtype t) { return t == SSD_F32 ? 4 : X_BV; }
+constexpr int fwd_steps(ssd_dtype t) { return t == SSD_F32 ? 8 : X_FS; }
+constexpr int bwd_steps(ssd_dtype t) { return t == SSD_F32 ? 4 : X_BS; }
 
-// ---- quads: four neighbouring channels of a row ------------------------------------------
-// Rows need only element alignment, so quads are loaded and stored as unaligned vectors
-// (one 8- or 16-byte access each; the hardware takes any alignment).
-template <typename T> struct Quad;
-template <> struct Quad<__bf16> {
-    uint2 v;
-    __device__ __forceinline__ float get(int i) const {
-        const uint32_t w = i < 2 ? v.x : v.y;
-        return __uint_as_float(i & 1 ? w & 0xffff0000u : w << 16);
-    }
-    __device__ __forceinline__ void clear() { v = make_uint2(0, 0); }
+// ---- pieces: a lane's V neighbouring channels of a row -------------------------------------
+// Rows need only element alignment, so pieces are loaded and stored as unaligned vectors (one
+// access each; the hardware takes any alignment).
+// Non-temporal, since every row is read and written once: at 4 x 4096 x 5120 in bf16 the
+// forward takes 98 us so and 110 us with cached accesses, the backward 188 and 219.
+template <int WORDS> using Words = uint32_t __attribute__((ext_vector_type(WORDS)));
+template <typename T, int WORDS> struct AnyWords {
+    typedef Words<WORDS> Any __attribute__((aligned(sizeof(T))));
 };
-template <> struct Quad<float> {
-    float4 v;
-    __device__ __forceinline__ float get(int i) const {
-        return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
-    }
-    __device__ __forceinline__ void clear() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
-};
-struct __attribute__((packed, aligned(2))) Bytes8 { uint32_t x, y; };
-struct __attribute__((packed, aligned(4))) Bytes16 { float x, y, z, w; };
-struct __attribute__((packed, aligned(1))) Bytes4 { uint32_t x; };
+struct __attribute__((packed, aligned(4))) Floats4 { float v[4]; };
 
-__device__ __forceinline__ void load(Quad<__bf16>& q, const __bf16* p) {
-    const Bytes8 b = *(const Bytes8*)p;
-    q.v = make_uint2(b.x, b.y);
+template <typename T, int V> struct Piece {
+    static constexpr int W = V * (int)sizeof(T) / 4;
+    uint32_t w[W];
+    __device__ __forceinline__ float get(int i) const {
+        if (sizeof(T) == 4) return __uint_as_float(w[i % W]);
+        return __uint_as_float(i & 1 ? w[i / 2] & 0xffff0000u : w[i / 2] << 16);
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = 0;
+    }
+    __device__ __forceinline__ void load(const T* p) {
+        const Words<W> b =
+            __builtin_nontemporal_load((const typename AnyWords<T, W>::Any*)p);
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = b[i];
+    }
+    // the first n < V channels, zeros behind them
+    __device__ __forceinline__ void load_part(const T* p, int n) {
+        clear();
+#pragma unroll
+        for (int i = 0; i < V - 1; ++i)
+            if (i < n) {
+                if (sizeof(T) == 4) w[i % W] = ((const uint32_t*)p)[i];
+                else w[i / 2] |= (uint32_t)((const uint16_t*)p)[i] << (16 * (i & 1));
+            }
+    }
+    // Values that a later pass computes from again: without this the compiler keeps the
+    // first pass' gates in registers instead, which halves the waves in flight.
+    __device__ __forceinline__ void renew() {
+#pragma unroll
+        for (int i = 0; i < W; ++i) asm volatile("" : "+v"(w[i]));
+    }
+};
+
+// Which channels a lane has.  Its piece starts at channel c0; it owns elements lo to hi of it.
+// A row's last piece is moved back to end with the row, so that every load is a whole piece
+// inside the row: a lane there computes channels that its neighbour owns too and stores its
+// own alone, and a lane behind the row's end owns none.  Rows narrower than a piece (NARROW)
+// have one lane, which loads element by element.
+struct Own {
+    int c0, lo, hi;
+    __device__ __forceinline__ bool any() const { return lo < hi; }
+    __device__ __forceinline__ bool has(int i) const { return i >= lo && i < hi; }
+};
+template <int V, bool NARROW> __device__ __forceinline__ Own own_of(int piece, int D) {
+    const int c = piece * V;
+    if (NARROW) return Own{0, 0, piece == 0 ? D : 0};
+    const int n = D - c;  // channels from c on
+    return Own{min(c, D - V), n >= V ? 0 : n > 0 ? V - n : V, V};
 }
-__device__ __forceinline__ void load(Quad<float>& q, const float* p) {
-    const Bytes16 b = *(const Bytes16*)p;
-    q.v = make_float4(b.x, b.y, b.z, b.w);
-}
-__device__ __forceinline__ void load_part(Quad<__bf16>& q, const __bf16* p, int n) {
-    const uint16_t* w = (const uint16_t*)p;
-    q.v = make_uint2(0, 0);
-    if (n > 0) q.v.x = w[0];
-    if (n > 1) q.v.x |= (uint32_t)w[1] << 16;
-    if (n > 2) q.v.y = w[2];
-}
-__device__ __forceinline__ void load_part(Quad<float>& q, const float* p, int n) {
-    q.v = make_float4(n > 0 ? p[0] : 0.f, n > 1 ? p[1] : 0.f, n > 2 ? p[2] : 0.f, 0.f);
-}
-// n: channels of the row from p on; four or more: the whole quad
-__device__ __forceinline__ void store(__bf16* p, const float (&v)[4], int n) {
-    typedef __bf16 pair __attribute__((ext_vector_type(2)));
-    union { pair h[2]; uint32_t w[2]; } u;
-    u.h[0] = pair{(__bf16)v[0], (__bf16)v[1]};
-    u.h[1] = pair{(__bf16)v[2], (__bf16)v[3]};
-    if (n >= 4) {
-        *(Bytes8*)p = Bytes8{u.w[0], u.w[1]};
+
+template <typename T, int V>
+__device__ __forceinline__ void store(T* p, const float (&v)[V], const Own& o) {
+    constexpr int W = V * (int)sizeof(T) / 4;
+    union { T t[V]; Words<W> b; } u;
+#pragma unroll
+    for (int i = 0; i < V; ++i) u.t[i] = from_f32<T>(v[i]);
+    if (o.hi - o.lo == V) {
+        __builtin_nontemporal_store(u.b, (typename AnyWords<T, W>::Any*)p);
     } else {
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (i < n) p[i] = u.h[i / 2][i % 2];
+        for (int i = 0; i < V; ++i)
+            if (o.has(i)) p[i] = u.t[i];
     }
 }
-__device__ __forceinline__ void store(float* p, const float (&v)[4], int n) {
-    if (n >= 4) {
-        *(Bytes16*)p = Bytes16{v[0], v[1], v[2], v[3]};
+template <int V, bool NARROW>
+__device__ __forceinline__ void load_f32(float (&v)[V], const float* p, const Own& o) {
+    if (!p) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = 0.f;
+    } else if (NARROW) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[i] = i < o.hi ? p[i] : 0.f;
     } else {
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
-            if (i < n) p[i] = v[i];
+        for (int i = 0; i < V; i += 4) {
+            const Floats4 f = *(const Floats4*)(p + i);
+            v[i] = f.v[0]; v[i + 1] = f.v[1]; v[i + 2] = f.v[2]; v[i + 3] = f.v[3];
+        }
     }
 }
-__device__ __forceinline__ void load4(float (&v)[4], const float* p, int n) {
+
+// A run's values of a tile's C = 16 V channels in LDS: column 64 (i / 4) + 4 lane + i % 4
+// holds channel V lane + i, so a lane's accesses are 16-byte vectors and neighbouring lanes'
+// lie side by side.
+template <int V> __device__ __forceinline__ void put(float* row, int cq, const float (&v)[V]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = p && i < n ? p[i] : 0.f;
+    for (int i = 0; i < V; i += 4)
+        *(float4*)(row + 16 * i + 4 * cq) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
 }
-__device__ __forceinline__ float4 lds4(const float* p) { return *(const float4*)p; }
-__device__ __forceinline__ void put4(float* p, const float (&v)[4]) {
-    *(float4*)p = make_float4(v[0], v[1], v[2], v[3]);
+template <int V> __device__ __forceinline__ void get(const float* row, int cq, float (&v)[V]) {
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+        const float4 f = *(const float4*)(row + 16 * i + 4 * cq);
+        v[i] = f.x; v[i + 1] = f.y; v[i + 2] = f.z; v[i + 3] = f.w;
+    }
+}
+// the channel of a column of tile column block cb, and whether its lane owns it
+template <int V, bool NARROW>
+__device__ __forceinline__ int channel_of(int cb, int col, int D, bool* owned) {
+    const Own o = own_of<V, NARROW>(cb * kLanes + col % 64 / 4, D);
+    const int i = col / 64 * 4 + col % 4;
+    *owned = o.has(i);
+    return o.c0 + i;  // inside the row, if not NARROW
 }
 
 // ---- tiles, and the carry between them ----------------------------------------------------
-constexpr int kBlockTiles = 16;  // tiles of a block of a chain
-constexpr int kLook = 4;         // spans looked at together
+constexpr int kBlockTiles = 16;  // tiles of a block of a chain, and blocks of a larger one
+// Counters of tiles taken, each for a range of neighbouring chains and on a cache line of its
+// own; one counter alone where there are too few chains to share them out evenly.
+constexpr unsigned kCounters = 8, kCounterWords = 64;
 
 struct Tiles {
-    unsigned* ticket;                  // counter of tiles taken (null: one tile per chain)
-    unsigned long long* span;          // [tile][2][64] the tile's P and H
-    unsigned long long* carry;         // [k / 16][chain][64] carry out of every 16th tile
+    unsigned* ticket;                  // the counters (null: one tile per chain)
+    unsigned long long* span;          // [tile][C] the tile's P (low word) and H
+    unsigned long long* block;         // [k / 16][chain][C] the same of 16 tiles
+    unsigned* carry;                   // [k / 256][chain][C] carry out of 256 tiles
     const uint8_t* starts;             // packed rows: bit t: a sequence starts at step t
+    const int* from;                   // and per byte of these: the first s with cu[s] >= 8 i
     int chains, blocks, nk;            // B * blocks, channel blocks, tiles of a chain
+    unsigned groups;                   // counters in use
 };
 
-// tag 1; 2: a sequence starts inside the span, so nothing from before reaches its end
-__device__ __forceinline__ void publish(unsigned long long* p, float v, unsigned tag) {
-    __hip_atomic_store(p, (unsigned long long)tag << 32 | __float_as_uint(v), __ATOMIC_RELAXED,
+// A word not yet published has all bits set: a NaN that no published value can be, since a
+// NaN is published as the one below.  A span is one 64-bit store, so it is seen whole.
+constexpr unsigned kNotYet = 0xffffffffu;
+__device__ __forceinline__ unsigned bits_of(float v) {
+    return v == v ? __float_as_uint(v) : 0x7fc00000u;
+}
+// P is a product of values in [0, 1]; kCut: a sequence starts inside the span, so nothing from
+// before reaches its end.
+constexpr float kCut = -1.f;
+__device__ __forceinline__ void publish(unsigned long long* p, float P, float H) {
+    __hip_atomic_store(p, (unsigned long long)bits_of(H) << 32 | bits_of(P), __ATOMIC_RELAXED,
                        __HIP_MEMORY_SCOPE_AGENT);
 }
-__device__ __forceinline__ unsigned long long look(const unsigned long long* p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ bool there(unsigned long long w) { return (w >> 32) != 0; }
-__device__ __forceinline__ float value(unsigned long long w) {
-    return __uint_as_float((unsigned)w);
+__device__ __forceinline__ void extend(float& P, float& H, float p, float h) {
+    H = p == kCut ? h : fmaf(p, H, h);
+    P = p == kCut || P == kCut ? kCut : P * p;
 }
 
-// One wave, a lane per channel.  (P, H): the tile's span; cut: a sequence starts inside;
-// first: the carry into the chain's first tile.  Returns the carry into this tile.  The
-// order of combining is fixed by the tile's place alone (the carry into its block, then the
-// block's earlier spans from first to last), never by what happens to be ready, so results
-// are the same bits on every run.
-__device__ float carry_in(const Tiles& tl, unsigned tile, int k, float P, float H, bool cut,
-                          float first) {
-    if (tl.nk == 1) return first;
-    const int lane = threadIdx.x & 63;
-    const int i = k % kBlockTiles;
-    const bool last = k == tl.nk - 1;
-    if (!last && i < kBlockTiles - 1) {
-        unsigned long long* s = tl.span + (size_t)tile * 2 * kCols + lane;
-        publish(s, P, cut ? 2 : 1);
-        publish(s + kCols, H, 1);
-    }
-    float accP = 1.f, accH = 0.f;
-    bool accCut = false;
-    const unsigned long long* s =
-        tl.span + (size_t)(tile - (unsigned)i * tl.chains) * 2 * kCols + lane;
-    const size_t step = (size_t)tl.chains * 2 * kCols;
-    for (int m0 = 0; m0 < i; m0 += kLook, s += kLook * step) {
-        unsigned long long p[kLook], h[kLook];
+// Fold n published spans, `step` words apart from s on, into (P, H), first to last.  A round of
+// loads for kLook of them, and further rounds for those that were not there yet.
+__device__ __forceinline__ void fold(const unsigned long long* s, size_t step, int n, float& P,
+                                     float& H) {
+    for (int m0 = 0; m0 < n; m0 += kLook, s += kLook * step) {
+        unsigned long long w[kLook];
+        unsigned missing = (1u << min(kLook, n - m0)) - 1;
         for (;;) {
-            bool all = true;
 #pragma unroll
             for (int m = 0; m < kLook; ++m)
-                if (m0 + m < i) {
-                    p[m] = look(s + m * step);
-                    h[m] = look(s + m * step + kCols);
-                }
+                if (missing >> m & 1)
+                    w[m] = __hip_atomic_load(s + m * step, __ATOMIC_RELAXED,
+                                             __HIP_MEMORY_SCOPE_AGENT);
 #pragma unroll
             for (int m = 0; m < kLook; ++m)
-                if (m0 + m < i) all = all && there(p[m]) && there(h[m]);
-            if (__all(all)) break;
+                if ((missing >> m & 1) && __all((unsigned)w[m] != kNotYet)) missing &= ~(1u << m);
+            if (!missing) break;
             __builtin_amdgcn_s_sleep(1);
         }
 #pragma unroll
         for (int m = 0; m < kLook; ++m)
-            if (m0 + m < i) {
-                const bool c = __builtin_amdgcn_readfirstlane((unsigned)(p[m] >> 32)) == 2;
-                accH = c ? value(h[m]) : fmaf(value(p[m]), accH, value(h[m]));
-                accP *= value(p[m]);
-                accCut = accCut || c;
-            }
+            if (m0 + m < n)
+                extend(P, H, __uint_as_float((unsigned)w[m]),
+                       __uint_as_float((unsigned)(w[m] >> 32)));
+    }
+}
+
+// One wave, a lane for column col of the tile's C; (P, H): the tile's span (P = kCut where a
+// sequence starts inside); first: the carry into the chain's first tile.  Publishes the
+// tile's span, behind 16 tiles what those amount to, and behind 256 the carry out of them;
+// returns the carry into this tile.  The order of combining is fixed by the tile's place
+// alone (the carry into its 256 tiles, the blocks of 16 before its own, the tiles of its own
+// block before it), never by what happens to be ready, so results are the same bits on every
+// run.
+template <int C>
+__device__ __forceinline__ float carry_in(const Tiles& tl, unsigned tile, int k, int col, float P,
+                                          float H, float first) {
+    if (tl.nk == 1) return first;
+    const bool last = k == tl.nk - 1;  // nobody looks at what it publishes
+    const int i = k % kBlockTiles, nb = k / kBlockTiles % kBlockTiles;
+    const int big = k / (kBlockTiles * kBlockTiles);
+    const size_t step = (size_t)tl.chains * C;
+    const size_t at = (size_t)(tile - (unsigned)k * tl.chains) * C + col;
+    if (!last && i < kBlockTiles - 1) publish(tl.span + k * step + at, P, H);
+    float bP = 1.f, bH = 0.f;  // the block up to this tile
+    fold(tl.span + (k - i) * step + at, step, i, bP, bH);
+    if (!last && i == kBlockTiles - 1 && nb < kBlockTiles - 1) {
+        float p = bP, h = bH;
+        extend(p, h, P, H);
+        publish(tl.block + (k / kBlockTiles) * step + at, p, h);
     }
     float in = first;
-    if (k >= kBlockTiles && !accCut) {
-        const unsigned long long* c =
-            tl.carry + ((size_t)(k / kBlockTiles - 1) * tl.chains + tile % tl.chains) * kCols + lane;
-        unsigned long long v;
-        while (!__all(there(v = look(c)))) __builtin_amdgcn_s_sleep(1);
-        in = value(v);
+    if (big > 0) {
+        const unsigned* c = tl.carry + (big - 1) * step + at;
+        unsigned v;
+        while (!__all((v = __hip_atomic_load(c, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)) !=
+                      kNotYet))
+            __builtin_amdgcn_s_sleep(1);
+        in = __uint_as_float(v);
     }
-    in = accCut ? accH : fmaf(accP, in, accH);
-    if (!last && i == kBlockTiles - 1)
-        publish(tl.carry + ((size_t)(k / kBlockTiles) * tl.chains + tile % tl.chains) * kCols + lane,
-                cut ? H : fmaf(P, in, H), 1);
+    if (nb > 0) {
+        float P16 = 1.f, H16 = 0.f;
+        fold(tl.block + (k / kBlockTiles - nb) * step + at, step, nb, P16, H16);
+        in = P16 == kCut ? H16 : fmaf(P16, in, H16);
+    }
+    in = bP == kCut ? bH : fmaf(bP, in, bH);
+    if (!last && i == kBlockTiles - 1 && nb == kBlockTiles - 1)
+        __hip_atomic_store(tl.carry + big * step + at, bits_of(P == kCut ? H : fmaf(P, in, H)),
+                           __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     return in;
 }
 
-// The sequence of a packed row whose last step is t.
-__device__ int sequence_ending(const int* cu, int nseq, int t) {
-    int lo = 0, hi = nseq - 1;  // first s with cu[s + 1] > t
-    while (lo < hi) {
-        const int m = (lo + hi) / 2;
-        if (cu[m + 1] > t) hi = m; else lo = m + 1;
-    }
-    return lo;
+// The sequence of a packed row whose last step is t; from: any s up to it with cu[s] <= t + 1.
+__device__ __forceinline__ int sequence_ending(const int* cu, int nseq, int from, int t) {
+    int s = from;  // to the first with cu[s] = t + 1: empty sequences lie behind it
+    while (s < nseq && cu[s] <= t) ++s;
+    return max(s - 1, 0);
+}
+
+// Tiles are taken from the counter of the workgroup's group; a workgroup takes its next
+// number while it works on a tile.
+struct Group {
+    unsigned* counter;
+    unsigned first, chains, tiles;  // the group's chains, and their tiles
+};
+__device__ __forceinline__ Group group_of(const Tiles& tl) {
+    const unsigned g = blockIdx.x % tl.groups, q = tl.chains / tl.groups,
+                   rem = tl.chains % tl.groups;
+    Group r;
+    r.counter = tl.ticket + g * kCounterWords;
+    r.first = g * q + min(g, rem);
+    r.chains = q + (g < rem ? 1 : 0);
+    r.tiles = r.chains * tl.nk;
+    return r;
+}
+
+// The workgroup's first number, and the number after t (in thread 0; without a counter, where
+// no tile waits for another, in all of them).
+__device__ __forceinline__ unsigned first_number(const Tiles& tl, const Group& g, unsigned* sh) {
+    if (!tl.ticket) return blockIdx.x / tl.groups;
+    if (threadIdx.x == 0) *sh = g.tiles ? atomicAdd(g.counter, 1u) : 0u;
+    __syncthreads();
+    return __builtin_amdgcn_readfirstlane(*sh);
+}
+__device__ __forceinline__ unsigned take_number(const Tiles& tl, const Group& g, unsigned t) {
+    if (!tl.ticket) return t + gridDim.x / tl.groups;
+    return threadIdx.x == 0 ? atomicAdd(g.counter, 1u) : 0u;
 }
 
 // Which tile, and where this thread stands in it.
 struct Place {
     unsigned tile;
-    int k, b, cb, cq, r, c0, n;  // n: channels of the row from c0 on (may be <= 0)
+    int k, b, cb, cq, r;
+    Own o;
 };
-__device__ __forceinline__ Place place(const Tiles& tl, int D, unsigned* shared) {
+// t: the number taken (uniform)
+template <int V, bool NARROW>
+__device__ __forceinline__ Place place(const Tiles& tl, const Group& g, unsigned t, int D) {
     Place p;
-    unsigned tile = blockIdx.x;
-    if (tl.ticket) {
-        if (threadIdx.x == 0) *shared = atomicAdd(tl.ticket, 1u);
-        __syncthreads();
-        tile = *shared;
-    }
-    p.tile = __builtin_amdgcn_readfirstlane(tile);
-    p.k = p.tile / tl.chains;
-    const int chain = p.tile % tl.chains;
+    p.k = t / g.chains;
+    const unsigned chain = g.first + t % g.chains;
+    p.tile = p.k * tl.chains + chain;
     p.b = chain / tl.blocks;
     p.cb = chain % tl.blocks;
-    p.cq = threadIdx.x & 15;
-    p.r = threadIdx.x >> 4;
-    p.c0 = p.cb * kCols + 4 * p.cq;
-    p.n = D - p.c0;
+    p.cq = threadIdx.x % kLanes;
+    p.r = threadIdx.x / kLanes;
+    p.o = own_of<V, NARROW>(p.cb * kLanes + p.cq, D);
     return p;
 }
 
-// Bits of a run's steps: starts (a sequence starts there) and ends (one ends there).
-template <int S>
-__device__ __forceinline__ void run_bits(const uint8_t* bits, int ts, int T, unsigned* starts,
-                                         unsigned* ends) {
-    const unsigned w = (bits[ts >> 3] | (unsigned)bits[(ts >> 3) + 1] << 8) >> (ts & 7);
-    constexpr unsigned mask = (1u << S) - 1;
-    *starts = w & mask;
-    *ends = (w >> 1) & mask;
-    if (T - 1 >= ts && T - 1 < ts + S) *ends |= 1u << (T - 1 - ts);
+// Where sequences of a packed row start and end among a run's steps.
+struct RunSeqs {
+    unsigned bits;  // of the starts, from the byte of the run's first step on
+    int from;       // first sequence that starts in that byte or behind
+    __device__ __forceinline__ void load(const Tiles& tl, int ts) {
+        bits = tl.starts[ts >> 3] | (unsigned)tl.starts[(ts >> 3) + 1] << 8;
+        from = tl.from[ts >> 3];
+    }
+    template <int S> __device__ __forceinline__ unsigned starts(int ts) const {
+        return bits >> (ts & 7) & ((1u << S) - 1);
+    }
+    template <int S> __device__ __forceinline__ unsigned ends(int ts, int T) const {
+        const unsigned e = bits >> (ts & 7) >> 1 & ((1u << S) - 1);
+        return T - 1 >= ts && T - 1 < ts + S ? e | 1u << (T - 1 - ts) : e;
+    }
+};
+
+// Byte offset of row `row` (of a tile) and channel c0 in rows `stride` elements apart: a
+// tile's rows lie within 2^31 bytes, so an address is a scalar base plus 32 bits per lane.
+template <typename T>
+__device__ __forceinline__ uint32_t row_offset(int row, long long stride, int c0) {
+    return ((uint32_t)row * (uint32_t)stride + (uint32_t)c0) * (uint32_t)sizeof(T);
 }
 
-// Load a run's quads of rows b*T + ts + j (steps behind T repeat the last one; the caller
-// clears them).
-template <typename T, int S>
-__device__ __forceinline__ void load_run(Quad<T> (&q)[S], const void* base, long long stride,
-                                         long long row0, int ts, int steps, int c0, int n) {
-    const T* p = (const T*)base + c0;
-    if (n >= 4) {
+// Load a run's pieces: step ts + j is the tile's row `run * S + j`; base: the tile's first
+// row; rows: the tile's rows that exist (steps behind repeat the last one; the caller clears
+// them).  No branch: one would make the loads of x wait for those of g.
+template <typename T, int V, int S, bool NARROW>
+__device__ __forceinline__ void load_run(Piece<T, V> (&q)[S], const void* base, long long stride,
+                                         int run, int rows, const Own& o) {
+    const uint32_t last = row_offset<T>(rows - 1, stride, o.c0);
+    uint32_t off = row_offset<T>(run * S, stride, o.c0);
+    const uint32_t step = (uint32_t)stride * (uint32_t)sizeof(T);
 #pragma unroll
-        for (int j = 0; j < S; ++j)
-            load(q[j], p + (row0 + min(ts + j, steps - 1)) * stride);
-    } else {
+    for (int j = 0; j < S; ++j, off += step) {
+        const T* p = (const T*)((const char*)base + min(off, last));
+        if (NARROW) q[j].load_part(p, o.hi);
+        else q[j].load(p);
+    }
+}
+
+// Codes and scales of a run's pieces: the 64 channels of a group are 64 / V neighbouring
+// lanes.  All of a wave's lanes take part.  row0: the tile's first row.
+template <typename T, int V, int S>
+__device__ __forceinline__ void pack_run(const Piece<T, V> (&v)[S], int8_t* codes, float* scales,
+                                         const GatedFwdArgs& a, const Place& w, long long row0,
+                                         int rows) {
+    const int groups = (a.D + SSD_CKPT_GROUP - 1) / SSD_CKPT_GROUP;
+    codes += row0 * a.D;
+    scales += row0 * groups;
+    const int piece = w.cb * kLanes + w.cq;
+    const uint32_t at = (uint32_t)(w.r * S) * (uint32_t)a.D + (uint32_t)w.o.c0;
+    const uint32_t sat =
+        (uint32_t)(w.r * S) * (uint32_t)groups + (uint32_t)(piece * V / SSD_CKPT_GROUP);
 #pragma unroll
-        for (int j = 0; j < S; ++j)
-            load_part(q[j], p + (row0 + min(ts + j, steps - 1)) * stride, n);
+    for (int j = 0; j < S; ++j) {
+        float f[V];
+        uint32_t most = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[i] = v[j].get(i);
+        if (w.o.hi - w.o.lo != V) {
+#pragma unroll
+            for (int i = 0; i < V; ++i)
+                if (!w.o.has(i)) f[i] = 0.f;  // another group's
+        }
+#pragma unroll
+        for (int i = 0; i < V; ++i) most = max(most, __float_as_uint(f[i]) & 0x7fffffffu);
+        const CkptScale s(ckpt_group_max<SSD_CKPT_GROUP / V>(most));
+        if (w.r * S + j >= rows || !w.o.any()) continue;
+        if (piece * V % SSD_CKPT_GROUP == 0) (scales + j * groups)[sat] = s.scale;
+        ckpt_store<V>(codes + (long long)j * a.D + at, f, s, w.o.lo, w.o.hi);
     }
 }
 
 // ---- forward ------------------------------------------------------------------------------
-template <typename T, int S, bool PACKED>
-__global__ __launch_bounds__(kTileThreads) void gated_fwd_kernel(GatedFwdArgs a, Tiles tl) {
-    constexpr int kTile = kRuns * S;
-    __shared__ __align__(16) float sP[kRuns * kCols], sH[kRuns * kCols], sE[kCols];
-    __shared__ unsigned sTile, sCut[kRuns];
-    const Place w = place(tl, a.D, &sTile);
-    const int t0 = w.k * kTile, ts = t0 + w.r * S;
-    const long long row0 = (long long)w.b * a.T;
-    Quad<T> x[S], g[S];
-    load_run<T, S>(g, a.g, a.g_stride, row0, ts, a.T, w.c0, w.n);
-    load_run<T, S>(x, a.x, a.x_stride, row0, ts, a.T, w.c0, w.n);
-    float bias[4];
-    load4(bias, a.bias ? a.bias + w.c0 : nullptr, w.n);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bias[i] *= kLog2e;
-    unsigned starts = 0, ends = 0;
-    if (PACKED) {
-        run_bits<S>(tl.starts, ts, a.T, &starts, &ends);
-        if (w.cq == 0) sCut[w.r] = starts;
-    }
-    const bool whole = t0 + kTile <= a.T;
-
-    float q[S][4], P[4] = {1.f, 1.f, 1.f, 1.f}, H[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[j][i] = gate_q(fmaf(g[j].get(i), kLog2e, bias[i]));
-    }
-    if (!whole) {
-#pragma unroll
-        for (int j = 0; j < S; ++j)
-            if (ts + j >= a.T) {
-                x[j].clear();
-                q[j][0] = q[j][1] = q[j][2] = q[j][3] = 0.f;
-            }
-    }
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-        if (PACKED && (starts >> j & 1)) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) P[i] = H[i] = 0.f;
+template <typename T, int V, int S, int RUNS, bool PACKED, bool CODES, bool NARROW>
+__global__ __launch_bounds__(RUNS * kLanes, 4) void gated_fwd_kernel(GatedFwdArgs a, Tiles tl) {
+    constexpr int C = kLanes * V, kTile = RUNS * S;
+    __shared__ __align__(16) float sP[RUNS * C], sH[RUNS * C], sE[C];
+    __shared__ unsigned sNext, sCut[RUNS];
+    const Group group = group_of(tl);
+    unsigned t = first_number(tl, group, &sNext);
+    if (t >= group.tiles) return;
+    Place w;
+    Piece<T, V> x[S], g[S];
+    float bias[V];
+    RunSeqs seqs;
+    auto fetch = [&]() {
+        w = place<V, NARROW>(tl, group, t, a.D);
+        const int t0 = w.k * kTile, rows = min(kTile, a.T - t0);
+        if (PACKED) seqs.load(tl, t0 + w.r * S);
+        const long long row0 = (long long)w.b * a.T + t0;
+        load_f32<V, NARROW>(bias, a.bias ? a.bias + w.o.c0 : nullptr, w.o);
+        load_run<T, V, S, NARROW>(g, (const T*)a.g + row0 * a.g_stride, a.g_stride, w.r, rows,
+                                  w.o);
+        load_run<T, V, S, NARROW>(x, (const T*)a.x + row0 * a.x_stride, a.x_stride, w.r, rows,
+                                  w.o);
+    };
+    fetch();
+    for (;;) {
+        const int t0 = w.k * kTile, ts = t0 + w.r * S;
+        const int rows = min(kTile, a.T - t0);
+        const bool whole = rows == kTile;
+        const long long row0 = (long long)w.b * a.T + t0;  // of the tile
+        const unsigned taken = take_number(tl, group, t);
+        unsigned starts = 0, ends = 0;
+        const int from = PACKED ? seqs.from : 0;
+        if (PACKED) {
+            starts = seqs.template starts<S>(ts);
+            ends = seqs.template ends<S>(ts, a.T);
+            if (w.cq == 0) sCut[w.r] = starts;
         }
+        float q[S][V];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            H[i] = gate_step(q[j][i], x[j].get(i), H[i]);
-            P[i] = fmaf(-q[j][i], P[i], P[i]);
+        for (int i = 0; i < V; ++i) bias[i] *= kLog2e;
+#pragma unroll
+        for (int j = 0; j < S; ++j) {
+#pragma unroll
+            for (int i = 0; i < V; ++i) q[j][i] = gate_q(fmaf(g[j].get(i), kLog2e, bias[i]));
         }
-    }
-    put4(&sP[w.r * kCols + 4 * w.cq], P);
-    put4(&sH[w.r * kCols + 4 * w.cq], H);
-    __syncthreads();
-    unsigned cuts = 0;
-    if (PACKED) cuts = (unsigned)__ballot(sCut[threadIdx.x & 31] != 0);
-    if (threadIdx.x < kCols) {
-        const int lane = threadIdx.x, c = w.cb * kCols + lane;
-        float accP = 1.f, accH = 0.f;
+        if (CODES) pack_run<T, V, S>(g, a.g_codes, a.g_scales, a, w, row0, rows);
+        if (!whole) {
 #pragma unroll
-        for (int r0 = 0; r0 < kRuns; r0 += 8) {
-            float p[8], h[8];
+            for (int j = 0; j < S; ++j)
+                if (ts + j >= a.T) {
+                    x[j].clear();
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                p[r] = sP[(r0 + r) * kCols + lane];
-                h[r] = sH[(r0 + r) * kCols + lane];
+                    for (int i = 0; i < V; ++i) q[j][i] = 0.f;
+                }
+        }
+        {
+            float P[V], H[V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) P[i] = 1.f, H[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                if (PACKED && (starts >> j & 1)) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) P[i] = H[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    H[i] = gate_step(q[j][i], x[j].get(i), H[i]);
+                    P[i] = fmaf(-q[j][i], P[i], P[i]);
+                }
+            }
+            put<V>(&sP[w.r * C], w.cq, P);
+            put<V>(&sH[w.r * C], w.cq, H);
+        }
+        if (threadIdx.x == 0) sNext = taken;
+        __syncthreads();
+        const unsigned next = __builtin_amdgcn_readfirstlane(sNext);
+        unsigned cuts = 0;
+        if (PACKED)
+            cuts = (unsigned)__ballot((threadIdx.x & 63) < RUNS && sCut[threadIdx.x % RUNS] != 0);
+        if (threadIdx.x < C) {
+            const int col = threadIdx.x;
+            float accP = 1.f, accH = 0.f;
+#pragma unroll
+            for (int r0 = 0; r0 < RUNS; r0 += kScan) {
+                float p[kScan], h[kScan];
+#pragma unroll
+                for (int r = 0; r < kScan; ++r) {
+                    p[r] = sP[(r0 + r) * C + col];
+                    h[r] = sH[(r0 + r) * C + col];
+                }
+#pragma unroll
+                for (int r = 0; r < kScan; ++r) {
+                    sP[(r0 + r) * C + col] = accP;
+                    sH[(r0 + r) * C + col] = accH;
+                    const bool cut = PACKED && (cuts >> (r0 + r) & 1);
+                    accH = cut ? h[r] : fmaf(p[r], accH, h[r]);
+                    accP *= p[r];
+                }
+            }
+            bool owned;
+            const int c = channel_of<V, NARROW>(w.cb, col, a.D, &owned);
+            const float first =
+                a.init && w.k < kBlockTiles * kBlockTiles && c < a.D
+                    ? a.init[(long long)w.b * a.D + c]
+                    : 0.f;
+            sE[col] = carry_in<C>(tl, w.tile, w.k, col, cuts ? kCut : accP, accH, first);
+        } else if (CODES) {  // meanwhile
+            pack_run<T, V, S>(x, a.x_codes, a.x_scales, a, w, row0, rows);
+        }
+        __syncthreads();
+        if (CODES && threadIdx.x < C)
+            pack_run<T, V, S>(x, a.x_codes, a.x_scales, a, w, row0, rows);
+        float h[V];
+        {
+            float p[V], e[V];
+            get<V>(&sH[w.r * C], w.cq, h);
+            get<V>(&sP[w.r * C], w.cq, p);
+            get<V>(sE, w.cq, e);
+            const bool cut = PACKED && (cuts & ((1u << w.r) - 1));
+#pragma unroll
+            for (int i = 0; i < V; ++i) h[i] = cut ? h[i] : fmaf(p[i], e[i], h[i]);
+        }
+        if (w.o.any()) {
+            if (a.entry && ts % kGatedChunk == 0 && ts < a.T) {
+                const long long nC = (a.T + kGatedChunk - 1) / kGatedChunk;
+                store<float, V>(a.entry + (w.b * nC + ts / kGatedChunk) * a.D + w.o.c0, h, w.o);
             }
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                sP[(r0 + r) * kCols + lane] = accP;
-                sH[(r0 + r) * kCols + lane] = accH;
-                const bool cut = PACKED && (cuts >> (r0 + r) & 1);
-                accH = cut ? h[r] : fmaf(p[r], accH, h[r]);
-                accP *= p[r];
+            for (int j = 0; j < S; ++j) {
+                if (PACKED && (starts >> j & 1)) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) h[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) h[i] = gate_step(q[j][i], x[j].get(i), h[i]);
+                if (whole || ts + j < a.T)
+                    store<T, V>((T*)((char*)((T*)a.h + (row0 + j) * a.D) +
+                                     row_offset<T>(w.r * S, a.D, w.o.c0)),
+                                h, w.o);
+                if (PACKED && a.final_state && (ends >> j & 1))
+                    store<float, V>(a.final_state +
+                                        (long long)sequence_ending(a.cu, a.nseq, from, ts + j) * a.D +
+                                        w.o.c0,
+                                    h, w.o);
             }
+            if (!PACKED && a.final_state && ts <= a.T - 1 && a.T - 1 < ts + S)
+                store<float, V>(a.final_state + (long long)w.b * a.D + w.o.c0, h, w.o);
         }
-        const float first =
-            w.k < kBlockTiles && a.init && c < a.D ? a.init[(long long)w.b * a.D + c] : 0.f;
-        sE[lane] = carry_in(tl, w.tile, w.k, accP, accH, cuts != 0, first);
+        t = next;
+        if (t >= group.tiles) break;
+        fetch();
+        __syncthreads();  // LDS is free again
     }
-    __syncthreads();
-    float h[4];
-    {
-        const float4 p = lds4(&sP[w.r * kCols + 4 * w.cq]), v = lds4(&sH[w.r * kCols + 4 * w.cq]);
-        const float4 e = lds4(&sE[4 * w.cq]);
-        const bool cut = PACKED && (cuts & ((1u << w.r) - 1));
-        h[0] = cut ? v.x : fmaf(p.x, e.x, v.x);
-        h[1] = cut ? v.y : fmaf(p.y, e.y, v.y);
-        h[2] = cut ? v.z : fmaf(p.z, e.z, v.z);
-        h[3] = cut ? v.w : fmaf(p.w, e.w, v.w);
-    }
-    if (w.n <= 0) return;
-    if (a.entry && ts % kGatedChunk == 0 && ts < a.T) {
-        const long long nC = (a.T + kGatedChunk - 1) / kGatedChunk;
-        store(a.entry + (w.b * nC + ts / kGatedChunk) * a.D + w.c0, h, w.n);
-    }
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-        if (PACKED && (starts >> j & 1)) h[0] = h[1] = h[2] = h[3] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) h[i] = gate_step(q[j][i], x[j].get(i), h[i]);
-        if (whole || ts + j < a.T)
-            store((T*)a.h + (row0 + ts + j) * a.D + w.c0, h, w.n);
-        if (PACKED && a.final_state && (ends >> j & 1))
-            store(a.final_state + (long long)sequence_ending(a.cu, a.nseq, ts + j) * a.D + w.c0, h,
-                  w.n);
-    }
-    if (!PACKED && a.final_state && ts <= a.T - 1 && a.T - 1 < ts + S)
-        store(a.final_state + (long long)w.b * a.D + w.c0, h, w.n);
-}
-
-// Values that a later pass computes from again: without this the compiler keeps the first
-// pass' gates in registers instead (205 against 128 and fewer, which halves the waves).
-__device__ __forceinline__ void renew(uint32_t& v) { asm volatile("" : "+v"(v)); }
-__device__ __forceinline__ void renew(Quad<__bf16>& q) { renew(q.v.x); renew(q.v.y); }
-__device__ __forceinline__ void renew(float& v) { asm volatile("" : "+v"(v)); }
-__device__ __forceinline__ void renew(Quad<float>& q) {
-    renew(q.v.x); renew(q.v.y); renew(q.v.z); renew(q.v.w);
 }
 
 // ---- backward -----------------------------------------------------------------------------
-// x and g of a run, from rows in T or from 8-bit codes and their scales (the tile's 64
-// channels are one group).
-template <typename T, int S, bool CODES> struct RunIn;
-template <typename T, int S> struct RunIn<T, S, false> {
-    Quad<T> v[S];
-    __device__ __forceinline__ void load(const void* rows, long long stride, const int8_t*,
-                                         const float*, long long row0, int ts, const Place& w,
-                                         const GatedBwdArgs& a) {
-        load_run<T, S>(v, rows, stride, row0, ts, a.T, w.c0, w.n);
+// x and g of a run, from rows in T or from 8-bit codes and their scales.
+template <typename T, int V, int S, bool CODES, bool NARROW> struct RunIn;
+template <typename T, int V, int S, bool NARROW> struct RunIn<T, V, S, false, NARROW> {
+    Piece<T, V> v[S];
+    __device__ __forceinline__ void load(const void* from, long long stride, const int8_t*,
+                                         const float*, long long row0, int rows, const Place& w,
+                                         int) {
+        load_run<T, V, S, NARROW>(v, (const T*)from + row0 * stride, stride, w.r, rows, w.o);
     }
     __device__ __forceinline__ float get(int j, int i) const { return v[j].get(i); }
     __device__ __forceinline__ void clear(int j) { v[j].clear(); }
     __device__ __forceinline__ void again() {
 #pragma unroll
-        for (int j = 0; j < S; ++j) renew(v[j]);
+        for (int j = 0; j < S; ++j) v[j].renew();
     }
 };
-template <typename T, int S> struct RunIn<T, S, true> {
-    uint32_t v[S];
+template <typename T, int V, int S, bool NARROW> struct RunIn<T, V, S, true, NARROW> {
+    CkptPiece<V> v[S];
     float s[S];
     __device__ __forceinline__ void load(const void*, long long, const int8_t* codes,
-                                         const float* scales, long long row0, int ts,
-                                         const Place& w, const GatedBwdArgs& a) {
-        const int groups = (a.D + kCols - 1) / kCols;
+                                         const float* scales, long long row0, int rows,
+                                         const Place& w, int D) {
+        const int groups = (D + SSD_CKPT_GROUP - 1) / SSD_CKPT_GROUP;
+        codes += row0 * D;
+        scales += row0 * groups;
+        const uint32_t group =
+            min((w.cb * kLanes + w.cq) * V / SSD_CKPT_GROUP, groups - 1);
 #pragma unroll
         for (int j = 0; j < S; ++j) {
-            const long long row = row0 + min(ts + j, a.T - 1);
-            const int8_t* p = codes + row * a.D + w.c0;
-            v[j] = 0;
-            if (w.n >= 4) {
-                v[j] = ((const Bytes4*)p)->x;
-            } else {
-#pragma unroll
-                for (int i = 0; i < 3; ++i)
-                    if (i < w.n) v[j] |= (uint32_t)(uint8_t)p[i] << (8 * i);
-            }
-            s[j] = scales[row * groups + w.cb];
+            const uint32_t row = min(w.r * S + j, rows - 1);
+            const int8_t* p = codes + (row * (uint32_t)D + (uint32_t)w.o.c0);
+            if (NARROW) v[j].load_part(p, w.o.hi);
+            else v[j].load(p);
+            s[j] = scales[row * (uint32_t)groups + group];
         }
     }
-    __device__ __forceinline__ float get(int j, int i) const {
-        return (float)(int8_t)(v[j] >> (8 * i)) * s[j];
-    }
-    __device__ __forceinline__ void clear(int j) { v[j] = 0; s[j] = 0.f; }
+    __device__ __forceinline__ float get(int j, int i) const { return v[j].get(i) * s[j]; }
+    __device__ __forceinline__ void clear(int j) { v[j].clear(); s[j] = 0.f; }
     __device__ __forceinline__ void again() {
 #pragma unroll
-        for (int j = 0; j < S; ++j) renew(v[j]);
+        for (int j = 0; j < S; ++j) v[j].renew();
     }
 };
 
-template <typename T, int S, bool PACKED, bool CODES>
-__global__ __launch_bounds__(kTileThreads) void gated_bwd_kernel(GatedBwdArgs a, Tiles tl,
-                                                                 float* part) {
-    constexpr int kTile = kRuns * S;
+template <typename T, int V, int S, int RUNS, bool PACKED, bool CODES, bool NARROW>
+__global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArgs a, Tiles tl,
+                                                                     float* part) {
+    constexpr int C = kLanes * V, kTile = RUNS * S;
     constexpr int kChunkRuns = kGatedChunk / S;
-    __shared__ __align__(16) float sP[kRuns * kCols], sH[kRuns * kCols], sC[kRuns * kCols],
-        sR[kRuns * kCols], sE[kCols];
-    __shared__ unsigned sTile, sCut[kRuns];
-    const Place w = place(tl, a.D, &sTile);
-    const int kt = tl.nk - 1 - w.k;  // last tile first
-    const int t0 = kt * kTile, ts = t0 + w.r * S;
-    const long long row0 = (long long)w.b * a.T;
-    RunIn<T, S, CODES> x, g;
-    Quad<T> dh[S];
-    g.load(a.g, a.g_stride, a.g_codes, a.g_scales, row0, ts, w, a);
-    x.load(a.x, a.x_stride, a.x_codes, a.x_scales, row0, ts, w, a);
-    load_run<T, S>(dh, a.dh, a.dh_stride, row0, ts, a.T, w.c0, w.n);
-    float bias[4];
-    load4(bias, a.bias ? a.bias + w.c0 : nullptr, w.n);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) bias[i] *= kLog2e;
-    unsigned starts = 0, ends = 0;
-    if (PACKED) {
-        run_bits<S>(tl.starts, ts, a.T, &starts, &ends);
-        if (w.cq == 0) sCut[w.r] = starts;
-    }
-    const bool whole = t0 + kTile <= a.T;
-    if (!whole) {
-#pragma unroll
-        for (int j = 0; j < S; ++j)
-            if (ts + j >= a.T) {
-                x.clear(j);
-                dh[j].clear();
-            }
-    }
-    // d_final of a packed sequence that ends at step j of this run
-    auto ending = [&](int j, float (&v)[4]) {
-        load4(v,
-              a.d_final ? a.d_final +
-                              (long long)sequence_ending(a.cu, a.nseq, ts + j) * a.D + w.c0
-                        : nullptr,
-              w.n);
+    static_assert(kTile % kGatedChunk == 0 && RUNS * kLanes >= 2 * C, "tiles hold whole chunks");
+    __shared__ __align__(16) float sP[RUNS * C], sH[RUNS * C], sC[RUNS * C], sR[RUNS * C], sE[C];
+    __shared__ unsigned sNext, sCut[RUNS];
+    const Group group = group_of(tl);
+    unsigned t = first_number(tl, group, &sNext);
+    if (t >= group.tiles) return;
+    Place w;
+    RunIn<T, V, S, CODES, NARROW> x, g;
+    Piece<T, V> dh[S];
+    float bias[V];
+    RunSeqs seqs;
+    auto fetch = [&]() {
+        w = place<V, NARROW>(tl, group, t, a.D);
+        const int t0 = (tl.nk - 1 - w.k) * kTile, rows = min(kTile, a.T - t0);  // last tile first
+        if (PACKED) seqs.load(tl, t0 + w.r * S);
+        const long long row0 = (long long)w.b * a.T + t0;
+        load_f32<V, NARROW>(bias, a.bias ? a.bias + w.o.c0 : nullptr, w.o);
+        g.load(a.g, a.g_stride, a.g_codes, a.g_scales, row0, rows, w, a.D);
+        x.load(a.x, a.x_stride, a.x_codes, a.x_scales, row0, rows, w, a.D);
+        load_run<T, V, S, NARROW>(dh, (const T*)a.dh + row0 * a.dh_stride, a.dh_stride, w.r, rows,
+                                  w.o);
     };
-    {
-        float P[4] = {1.f, 1.f, 1.f, 1.f}, H[4] = {0.f, 0.f, 0.f, 0.f}, C[4];
-        float q[S][4];
+    fetch();
+    for (;;) {
+        const int kt = tl.nk - 1 - w.k;
+        const int t0 = kt * kTile, ts = t0 + w.r * S;
+        const int rows = min(kTile, a.T - t0);
+        const bool whole = rows == kTile;
+        const long long row0 = (long long)w.b * a.T + t0;  // of the tile
+        const unsigned taken = take_number(tl, group, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) bias[i] *= kLog2e;
+        unsigned starts = 0, ends = 0;
+        const int from = PACKED ? seqs.from : 0;
+        if (PACKED) {
+            starts = seqs.template starts<S>(ts);
+            ends = seqs.template ends<S>(ts, a.T);
+            if (w.cq == 0) sCut[w.r] = starts;
+        }
+        if (!whole) {
+#pragma unroll
+            for (int j = 0; j < S; ++j)
+                if (ts + j >= a.T) {
+                    x.clear(j);
+                    dh[j].clear();
+                }
+        }
+        // d_final of a packed sequence that ends at step j of this run
+        auto ending = [&](int j, float (&v)[V]) {
+            load_f32<V, NARROW>(
+                v,
+                a.d_final
+                    ? a.d_final + (long long)sequence_ending(a.cu, a.nseq, from, ts + j) * a.D + w.o.c0
+                    : nullptr,
+                w.o);
+        };
+        {
+            float P[V], H[V], G[V], q[S][V];
+#pragma unroll
+            for (int i = 0; i < V; ++i) P[i] = 1.f, H[i] = G[i] = 0.f;
+#pragma unroll
+            for (int j = 0; j < S; ++j) {
+                if (PACKED && (starts >> j & 1)) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) P[i] = H[i] = 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    q[j][i] = gate_q(fmaf(g.get(j, i), kLog2e, bias[i]));
+                    if (!whole && ts + j >= a.T) q[j][i] = 0.f;
+                    H[i] = gate_step(q[j][i], x.get(j, i), H[i]);
+                    P[i] = fmaf(-q[j][i], P[i], P[i]);
+                }
+            }
+#pragma unroll
+            for (int j = S - 1; j >= 0; --j) {
+                if (PACKED && (ends >> j & 1)) ending(j, G);
+#pragma unroll
+                for (int i = 0; i < V; ++i) {
+                    const float v = dh[j].get(i) + G[i];
+                    G[i] = PACKED && (starts >> j & 1) ? 0.f : fmaf(-q[j][i], v, v);
+                }
+            }
+            put<V>(&sP[w.r * C], w.cq, P);
+            put<V>(&sH[w.r * C], w.cq, H);
+            put<V>(&sC[w.r * C], w.cq, G);
+        }
+        if (threadIdx.x == 0) sNext = taken;
+        __syncthreads();
+        const unsigned next = __builtin_amdgcn_readfirstlane(sNext);
+        unsigned cuts = 0;
+        if (PACKED)
+            cuts = (unsigned)__ballot((threadIdx.x & 63) < RUNS && sCut[threadIdx.x % RUNS] != 0);
+        if (threadIdx.x < C) {  // the first waves: G, last run first
+            const int col = threadIdx.x;
+            float accP = 1.f, accC = 0.f;
+#pragma unroll
+            for (int r0 = RUNS - kScan; r0 >= 0; r0 -= kScan) {
+                float p[kScan], v[kScan];
+#pragma unroll
+                for (int r = 0; r < kScan; ++r) {
+                    p[r] = sP[(r0 + r) * C + col];
+                    v[r] = sC[(r0 + r) * C + col];
+                }
+#pragma unroll
+                for (int r = kScan - 1; r >= 0; --r) {
+                    sR[(r0 + r) * C + col] = accP;
+                    sC[(r0 + r) * C + col] = accC;
+                    const bool cut = PACKED && (cuts >> (r0 + r) & 1);
+                    accC = cut ? v[r] : fmaf(p[r], accC, v[r]);
+                    accP *= p[r];
+                }
+            }
+            bool owned;
+            const int c = channel_of<V, NARROW>(w.cb, col, a.D, &owned);
+            const float first =
+                !PACKED && a.d_final && w.k < kBlockTiles * kBlockTiles && c < a.D
+                    ? a.d_final[(long long)w.b * a.D + c]
+                    : 0.f;
+            sE[col] = carry_in<C>(tl, w.tile, w.k, col, cuts ? kCut : accP, accC, first);
+        } else if (threadIdx.x < 2 * C) {  // the next: h, from every chunk's entry state
+            const int col = threadIdx.x - C;
+            bool owned;
+            const int c = channel_of<V, NARROW>(w.cb, col, a.D, &owned);
+            const int nC = (a.T + kGatedChunk - 1) / kGatedChunk;
+            float E[kTile / kGatedChunk];
+#pragma unroll
+            for (int k = 0; k < kTile / kGatedChunk; ++k) {
+                const int chunk = t0 / kGatedChunk + k;
+                E[k] = chunk < nC && c < a.D ? a.entry[((long long)w.b * nC + chunk) * a.D + c]
+                                             : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < kTile / kGatedChunk; ++k) {
+                float e = E[k];
+#pragma unroll
+                for (int r = k * kChunkRuns; r < (k + 1) * kChunkRuns; ++r) {
+                    const float p = sP[r * C + col], v = sH[r * C + col];
+                    sH[r * C + col] = e;
+                    e = PACKED && (cuts >> r & 1) ? v : fmaf(p, e, v);
+                }
+            }
+        }
+        __syncthreads();
+        float h[V], G[V], db[V];
+        {
+            float p[V], in[V];
+            get<V>(&sH[w.r * C], w.cq, h);
+            get<V>(&sC[w.r * C], w.cq, G);
+            get<V>(&sR[w.r * C], w.cq, p);
+            get<V>(sE, w.cq, in);
+            const bool cut = PACKED && w.r < RUNS - 1 && (cuts >> (w.r + 1));
+#pragma unroll
+            for (int i = 0; i < V; ++i) {
+                G[i] = cut ? G[i] : fmaf(p[i], in[i], G[i]);
+                db[i] = 0.f;
+            }
+        }
+        g.again();
+        x.again();
+#pragma unroll
+        for (int j = 0; j < S; ++j) dh[j].renew();
+        float off[S][V];  // h_{t-1} - x_t
 #pragma unroll
         for (int j = 0; j < S; ++j) {
             if (PACKED && (starts >> j & 1)) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) P[i] = H[i] = 0.f;
+                for (int i = 0; i < V; ++i) h[i] = 0.f;
             }
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                q[j][i] = gate_q(fmaf(g.get(j, i), kLog2e, bias[i]));
-                if (!whole && ts + j >= a.T) q[j][i] = 0.f;
-                H[i] = gate_step(q[j][i], x.get(j, i), H[i]);
-                P[i] = fmaf(-q[j][i], P[i], P[i]);
+            for (int i = 0; i < V; ++i) {
+                off[j][i] = h[i] - x.get(j, i);
+                if (j < S - 1) {
+                    const float q = gate_q(fmaf(g.get(j, i), kLog2e, bias[i]));
+                    h[i] = fmaf(-q, off[j][i], h[i]);
+                }
             }
         }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) C[i] = 0.f;
+        g.again();
 #pragma unroll
         for (int j = S - 1; j >= 0; --j) {
-            if (PACKED && (ends >> j & 1)) ending(j, C);
+            if (PACKED && (ends >> j & 1)) ending(j, G);
+            if (whole || ts + j < a.T) {
+                float dx[V], dg[V];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float G = dh[j].get(i) + C[i];
-                C[i] = fmaf(-q[j][i], G, G);
-            }
-            if (PACKED && (starts >> j & 1)) C[0] = C[1] = C[2] = C[3] = 0.f;
-        }
-        put4(&sP[w.r * kCols + 4 * w.cq], P);
-        put4(&sH[w.r * kCols + 4 * w.cq], H);
-        put4(&sC[w.r * kCols + 4 * w.cq], C);
-    }
-    __syncthreads();
-    unsigned cuts = 0;
-    if (PACKED) cuts = (unsigned)__ballot(sCut[threadIdx.x & 31] != 0);
-    if (threadIdx.x < kCols) {  // the first wave: G, last run first
-        const int lane = threadIdx.x, c = w.cb * kCols + lane;
-        float accP = 1.f, accC = 0.f;
-#pragma unroll
-        for (int r0 = kRuns - 8; r0 >= 0; r0 -= 8) {
-            float p[8], v[8];
-#pragma unroll
-            for (int r = 0; r < 8; ++r) {
-                p[r] = sP[(r0 + r) * kCols + lane];
-                v[r] = sC[(r0 + r) * kCols + lane];
-            }
-#pragma unroll
-            for (int r = 7; r >= 0; --r) {
-                sR[(r0 + r) * kCols + lane] = accP;
-                sC[(r0 + r) * kCols + lane] = accC;
-                const bool cut = PACKED && (cuts >> (r0 + r) & 1);
-                accC = cut ? v[r] : fmaf(p[r], accC, v[r]);
-                accP *= p[r];
+                for (int i = 0; i < V; ++i) {
+                    const Gate e(fmaf(g.get(j, i), kLog2e, bias[i]));
+                    const float v = dh[j].get(i) + G[i];
+                    dx[i] = e.q * v;
+                    dg[i] = dx[i] * e.a * off[j][i];
+                    db[i] += dg[i];
+                    G[i] = PACKED && (starts >> j & 1) ? 0.f : fmaf(-e.q, v, v);
+                }
+                store<T, V>((T*)((char*)((T*)a.dx + (row0 + j) * a.dx_stride) +
+                                 row_offset<T>(w.r * S, a.dx_stride, w.o.c0)),
+                            dx, w.o);
+                store<T, V>((T*)((char*)((T*)a.dg + (row0 + j) * a.dg_stride) +
+                                 row_offset<T>(w.r * S, a.dg_stride, w.o.c0)),
+                            dg, w.o);
             }
         }
-        const float first = !PACKED && w.k < kBlockTiles && a.d_final && c < a.D
-                                ? a.d_final[(long long)w.b * a.D + c]
-                                : 0.f;
-        sE[lane] = carry_in(tl, w.tile, w.k, accP, accC, cuts != 0, first);
-    } else if (threadIdx.x < 2 * kCols) {  // the second: h, from every chunk's entry state
-        const int lane = threadIdx.x - kCols, c = w.cb * kCols + lane;
-        const int nC = (a.T + kGatedChunk - 1) / kGatedChunk;
-        float E[kTile / kGatedChunk];
+        if (!PACKED && a.d_init && ts == 0)
+            store<float, V>(a.d_init + (long long)w.b * a.D + w.o.c0, G, w.o);
+        const Place done = w;
+        t = next;
+        const bool more = t < group.tiles;
+        if (more) fetch();
+        if (part) {
+            put<V>(&sP[done.r * C], done.cq, db);  // the scans are done with sP
+            __syncthreads();
+            if (threadIdx.x < C) {
+                bool owned;
+                const int c = channel_of<V, NARROW>(done.cb, threadIdx.x, a.D, &owned);
+                float s = 0.f;
 #pragma unroll
-        for (int k = 0; k < kTile / kGatedChunk; ++k) {
-            const int chunk = t0 / kGatedChunk + k;
-            E[k] = chunk < nC && c < a.D ? a.entry[((long long)w.b * nC + chunk) * a.D + c] : 0.f;
-        }
-#pragma unroll
-        for (int k = 0; k < kTile / kGatedChunk; ++k) {
-            float e = E[k];
-#pragma unroll
-            for (int r = k * kChunkRuns; r < (k + 1) * kChunkRuns; ++r) {
-                const float p = sP[r * kCols + lane], v = sH[r * kCols + lane];
-                sH[r * kCols + lane] = e;
-                e = PACKED && (cuts >> r & 1) ? v : fmaf(p, e, v);
+                for (int r = 0; r < RUNS; ++r) s += sP[r * C + threadIdx.x];
+                if (owned) part[((long long)done.b * tl.nk + kt) * a.D + c] = s;
             }
         }
-    }
-    __syncthreads();
-    float h[4], C[4], db[4] = {0.f, 0.f, 0.f, 0.f};
-    {
-        const int at = w.r * kCols + 4 * w.cq;
-        const float4 e = lds4(&sH[at]), p = lds4(&sR[at]), v = lds4(&sC[at]);
-        const float4 in = lds4(&sE[4 * w.cq]);
-        h[0] = e.x; h[1] = e.y; h[2] = e.z; h[3] = e.w;
-        const bool cut = PACKED && w.r < 31 && (cuts >> (w.r + 1));
-        C[0] = cut ? v.x : fmaf(p.x, in.x, v.x);
-        C[1] = cut ? v.y : fmaf(p.y, in.y, v.y);
-        C[2] = cut ? v.z : fmaf(p.z, in.z, v.z);
-        C[3] = cut ? v.w : fmaf(p.w, in.w, v.w);
-    }
-    g.again();
-    x.again();
-#pragma unroll
-    for (int j = 0; j < S; ++j) renew(dh[j]);
-    float off[S][4];  // h_{t-1} - x_t
-#pragma unroll
-    for (int j = 0; j < S; ++j) {
-        if (PACKED && (starts >> j & 1)) h[0] = h[1] = h[2] = h[3] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            off[j][i] = h[i] - x.get(j, i);
-            if (j < S - 1) {
-                const float q = gate_q(fmaf(g.get(j, i), kLog2e, bias[i]));
-                h[i] = fmaf(-q, off[j][i], h[i]);
-            }
-        }
-    }
-    g.again();
-#pragma unroll
-    for (int j = S - 1; j >= 0; --j) {
-        if (PACKED && (ends >> j & 1)) ending(j, C);
-        if (whole || ts + j < a.T) {
-            float dx[4], dg[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const Gate e(fmaf(g.get(j, i), kLog2e, bias[i]));
-                const float G = dh[j].get(i) + C[i];
-                dx[i] = e.q * G;
-                dg[i] = dx[i] * e.a * off[j][i];
-                db[i] += dg[i];
-                C[i] = fmaf(-e.q, G, G);
-            }
-            const long long row = row0 + ts + j;
-            store((T*)a.dx + row * a.dx_stride + w.c0, dx, w.n);
-            store((T*)a.dg + row * a.dg_stride + w.c0, dg, w.n);
-        }
-        if (PACKED && (starts >> j & 1)) C[0] = C[1] = C[2] = C[3] = 0.f;
-    }
-    if (!PACKED && a.d_init && ts == 0) store(a.d_init + (long long)w.b * a.D + w.c0, C, w.n);
-    if (!part) return;
-    put4(&sP[w.r * kCols + 4 * w.cq], db);  // the scans are done with sP
-    __syncthreads();
-    if (threadIdx.x < kCols && w.cb * kCols + (int)threadIdx.x < a.D) {
-        float s = 0.f;
-#pragma unroll
-        for (int r = 0; r < kRuns; ++r) s += sP[r * kCols + threadIdx.x];
-        part[((long long)w.b * tl.nk + kt) * a.D + w.cb * kCols + threadIdx.x] = s;
+        if (!more) break;
+        __syncthreads();  // LDS is free again
     }
 }
 
 // ---- small kernels ------------------------------------------------------------------------
 constexpr int kThreads = 256;
 
-// Before a pass: the counter and the tags cleared, the start bits of a packed row, and zero
+// Before a pass: the counters cleared, spans and carries marked missing, the start bits of a packed row, and zero
 // final states for its empty sequences.
 struct Prep {
-    unsigned* clear;       // ticket and tags: words to clear
-    long long words;
+    unsigned* clear;       // counters, then spans and carries: words to set
+    long long zeros, words;  // the first to 0, the others to kNotYet
     uint8_t* starts;       // null: not a packed row
-    int bytes;             // of starts
+    int* from;
+    int bytes;             // of starts; words of from
     const int* cu;
     int nseq, T, D;
     float* final_state;    // null: none
@@ -631,7 +867,8 @@ __global__ __launch_bounds__(kThreads) void gated_prep_kernel(Prep p) {
     const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
     const long long all = (long long)gridDim.x * kThreads;
     for (long long i = id; i < p.words / 4; i += all)
-        reinterpret_cast<uint4*>(p.clear)[i] = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint4*>(p.clear)[i] = i < p.zeros / 4 ? make_uint4(0, 0, 0, 0)
+                                                       : make_uint4(~0u, ~0u, ~0u, ~0u);
     if (!p.starts) return;
     for (long long i = id; i < p.bytes; i += all) {
         int lo = 0, hi = p.nseq;  // first s with cu[s] >= 8 i
@@ -643,6 +880,7 @@ __global__ __launch_bounds__(kThreads) void gated_prep_kernel(Prep p) {
         for (int s = lo; s < p.nseq && p.cu[s] < 8 * i + 8; ++s)
             if (p.cu[s + 1] > p.cu[s]) bits |= 1u << (p.cu[s] - 8 * i);
         p.starts[i] = (uint8_t)bits;
+        p.from[i] = lo;
     }
     if (!p.final_state) return;
     for (long long i = id; i < (long long)p.nseq * p.D; i += all) {
@@ -655,9 +893,9 @@ __global__ __launch_bounds__(kThreads) void gated_prep_kernel(Prep p) {
 // order.
 __global__ __launch_bounds__(1024) void gated_dbias_kernel(const float* part, float* d_bias,
                                                            int rows, int D) {
-    __shared__ float s[16][kCols];
+    __shared__ float s[16][64];
     const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int c = blockIdx.x * kCols + lane;
+    const int c = blockIdx.x * 64 + lane;
     float v = 0.f;
     if (c < D)
         for (int r = w; r < rows; r += 16) v += part[(long long)r * D + c];
@@ -689,37 +927,50 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedStepArgs a) {
 
 unsigned blocks_of(long long n) { return (unsigned)((n + kThreads - 1) / kThreads); }
 
-// ---- workspace: ticket and tags | start bits | d_bias' sums ---------------------------------
+// ---- workspace: counters and spans | start bits, sequences | d_bias' sums -------------------------------
 struct Layout {
     int nk, blocks;
-    long long tiles, carries;
+    long long tiles, spans, carries;  // tiles; spans of one and of 16; carries
     size_t clear, starts, part, bytes;  // sizes of the first two; offset of the third; total
 };
+constexpr size_t kCounterBytes = kCounters * kCounterWords * 4;
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
-Layout layout(int B, int T, int D, int steps) {
+// tiles of `steps` steps and `cols` channels
+Layout layout(int B, int T, int D, int steps, int cols) {
     Layout l;
-    const int kTile = kRuns * steps;
-    l.nk = (T + kTile - 1) / kTile;
-    l.blocks = (D + kCols - 1) / kCols;
+    l.nk = (T + steps - 1) / steps;
+    l.blocks = (D + cols - 1) / cols;
     l.tiles = (long long)B * l.blocks * l.nk;
-    l.carries = l.nk / kBlockTiles * (l.tiles / l.nk);
-    l.clear = l.nk > 1 ? 256 + ((size_t)l.tiles * 2 + l.carries) * kCols * 8 : 0;
-    l.starts = up256((size_t)l.nk * (kTile / 8) + 1);
-    l.part = l.clear + l.starts;
+    const long long chains = (long long)B * l.blocks;
+    l.spans = l.tiles + chains * (l.nk / kBlockTiles);
+    l.carries = (chains * (l.nk / (kBlockTiles * kBlockTiles)) + 1) / 2 * 2;
+    l.clear = kCounterBytes +
+              (l.nk > 1 ? (size_t)(l.spans * 2 + l.carries) * cols * sizeof(unsigned) : 0);
+    l.starts = up256((size_t)l.nk * ((steps + 7) / 8) + 1);
+    l.part = l.clear + l.starts * 5;
     l.bytes = l.part + (size_t)B * l.nk * D * sizeof(float);
     return l;
 }
-Tiles tiles_of(const Layout& l, int B, char* ws, bool packed) {
+Layout fwd_layout(ssd_dtype dtype, int B, int T, int D) {
+    return layout(B, T, D, kFwdRuns * fwd_steps(dtype), kLanes * fwd_vec(dtype));
+}
+Layout bwd_layout(ssd_dtype dtype, int B, int T, int D) {
+    return layout(B, T, D, kBwdRuns * bwd_steps(dtype), kLanes * bwd_vec(dtype));
+}
+Tiles tiles_of(const Layout& l, int B, int cols, char* ws, bool packed) {
     Tiles t = {};
     t.blocks = l.blocks;
     t.chains = B * l.blocks;
     t.nk = l.nk;
-    if (l.nk > 1) {
-        t.ticket = (unsigned*)ws;
-        t.span = (unsigned long long*)(ws + 256);
-        t.carry = t.span + l.tiles * 2 * kCols;
+    t.groups = t.chains >= 8 * (int)kCounters ? kCounters : 1;
+    if (l.nk > 1) t.ticket = (unsigned*)ws;
+    t.span = (unsigned long long*)(ws + kCounterBytes);
+    t.block = t.span + l.tiles * cols;
+    t.carry = (unsigned*)(t.span + l.spans * cols);
+    if (packed) {
+        t.starts = (const uint8_t*)(ws + l.clear);
+        t.from = (const int*)(ws + l.clear + l.starts);
     }
-    if (packed) t.starts = (const uint8_t*)(ws + l.clear);
     return t;
 }
 hipError_t prepare(const Layout& l, char* ws, const int* cu, int nseq, int T, int D,
@@ -727,11 +978,13 @@ hipError_t prepare(const Layout& l, char* ws, const int* cu, int nseq, int T, in
     if (l.nk <= 1 && !cu) return hipSuccess;
     Prep p = {};
     p.clear = (unsigned*)ws;
+    p.zeros = kCounters * kCounterWords;
     p.words = (long long)(l.clear / 4);
     long long work = p.words / 4;
     if (cu) {
         p.starts = (uint8_t*)(ws + l.clear);
         p.bytes = (int)l.starts;
+        p.from = (int*)(ws + l.clear + l.starts);
         p.cu = cu; p.nseq = nseq; p.T = T; p.D = D;
         p.final_state = final_state;
         if (p.bytes > work) work = p.bytes;
@@ -747,68 +1000,89 @@ hipError_t prepare(const Layout& l, char* ws, const int* cu, int nseq, int T, in
 
 size_t gated_workspace_bytes(int B, int T, int D) {
     if (B == 0 || T == 0 || D == 0) return 0;
-    const size_t fwd = layout(B, T, D, kFwdSteps).bytes;
-    const size_t bwd = layout(B, T, D, bwd_steps(SSD_F32)).bytes;  // the shorter tiles
-    return fwd > bwd ? fwd : bwd;
+    size_t most = 0;
+    for (ssd_dtype t : {SSD_F32, SSD_BF16})
+        for (const Layout& l : {fwd_layout(t, B, T, D), bwd_layout(t, B, T, D)})
+            if (l.bytes > most) most = l.bytes;
+    return most;
 }
 
+namespace {
+// As many workgroups as are resident at once, and no more per counter than its tiles.
+template <int RUNS, auto kern, typename... Args>
+hipError_t launch_tiles(const Tiles& tl, hipStream_t st, Args... args) {
+    static DeviceSlots slots;
+    int grid = 0;
+    const hipError_t e =
+        resident_grid((const void*)kern, RUNS * kLanes, 0, slots, &grid);
+    if (e != hipSuccess) return e;
+    const long long most =
+        ((long long)tl.chains + tl.groups - 1) / tl.groups * tl.nk * tl.groups;
+    if (grid > most) grid = (int)most;
+    kern<<<grid, RUNS * kLanes, 0, st>>>(args...);
+    return hipGetLastError();
+}
+
+template <typename T, ssd_dtype DT, bool NARROW>
+hipError_t run_fwd(const GatedFwdArgs& a, char* ws, hipStream_t st) {
+    constexpr int V = fwd_vec(DT), S = fwd_steps(DT);
+    const Layout l = fwd_layout(DT, a.B, a.T, a.D);
+    hipError_t e = prepare(l, ws, a.cu, a.nseq, a.T, a.D, a.final_state, st);
+    if (e != hipSuccess) return e;
+    const Tiles tl = tiles_of(l, a.B, kLanes * V, ws, a.cu != nullptr);
+    const bool codes = a.x_codes != nullptr;
+#define SSD_GATED_FWD(PACKED, CODES) \
+    launch_tiles<kFwdRuns, gated_fwd_kernel<T, V, S, kFwdRuns, PACKED, CODES, NARROW>>(tl, st, a, tl)
+    if (a.cu) return codes ? SSD_GATED_FWD(true, true) : SSD_GATED_FWD(true, false);
+    return codes ? SSD_GATED_FWD(false, true) : SSD_GATED_FWD(false, false);
+#undef SSD_GATED_FWD
+}
+
+template <typename T, ssd_dtype DT, bool NARROW>
+hipError_t run_bwd(const GatedBwdArgs& a, char* ws, hipStream_t st) {
+    constexpr int V = bwd_vec(DT), S = bwd_steps(DT);
+    const Layout l = bwd_layout(DT, a.B, a.T, a.D);
+    hipError_t e = prepare(l, ws, a.cu, a.nseq, a.T, a.D, nullptr, st);
+    if (e != hipSuccess) return e;
+    const Tiles tl = tiles_of(l, a.B, kLanes * V, ws, a.cu != nullptr);
+    const int rows = a.B * l.nk;
+    float* part = !a.d_bias ? nullptr : rows == 1 ? a.d_bias : (float*)(ws + l.part);
+    const bool codes = a.x_codes != nullptr;
+#define SSD_GATED_BWD(PACKED, CODES) \
+    launch_tiles<kBwdRuns, gated_bwd_kernel<T, V, S, kBwdRuns, PACKED, CODES, NARROW>>(tl, st, a, tl, part)
+    if (a.cu) e = codes ? SSD_GATED_BWD(true, true) : SSD_GATED_BWD(true, false);
+    else e = codes ? SSD_GATED_BWD(false, true) : SSD_GATED_BWD(false, false);
+#undef SSD_GATED_BWD
+    if (e != hipSuccess || !a.d_bias || rows == 1) return e;
+    gated_dbias_kernel<<<(unsigned)((a.D + 63) / 64), 1024, 0, st>>>(part, a.d_bias, rows, a.D);
+    return hipGetLastError();
+}
+
+// fn<T, dtype, NARROW>(a, ws, st): rows narrower than a piece have forms of their own
+#define SSD_GATED_RUN(fn, vec)                                                         \
+    (dtype == SSD_F32 ? (a.D < vec(SSD_F32) ? fn<float, SSD_F32, true>(a, (char*)ws, st)      \
+                                            : fn<float, SSD_F32, false>(a, (char*)ws, st))    \
+                      : (a.D < vec(SSD_BF16) ? fn<__bf16, SSD_BF16, true>(a, (char*)ws, st)   \
+                                             : fn<__bf16, SSD_BF16, false>(a, (char*)ws, st)))
+}  // namespace
+
 hipError_t launch_gated_fwd(ssd_dtype dtype, const GatedFwdArgs& a, void* ws, hipStream_t st) {
-    if (a.T == 0) {
-        if (!a.final_state) return hipSuccess;
-        const long long n = (long long)(a.cu ? a.nseq : a.B) * a.D;
-        gated_carry_kernel<<<blocks_of(n), kThreads, 0, st>>>(a.init, a.final_state, n);
-        return hipGetLastError();
-    }
-    const Layout l = layout(a.B, a.T, a.D, kFwdSteps);
-    hipError_t e = prepare(l, (char*)ws, a.cu, a.nseq, a.T, a.D, a.final_state, st);
-    if (e != hipSuccess) return e;
-    const Tiles tl = tiles_of(l, a.B, (char*)ws, a.cu != nullptr);
-    const dim3 grid((unsigned)l.tiles), block(kTileThreads);
-    constexpr int S = kFwdSteps;
-    if (dtype == SSD_F32)
-        a.cu ? gated_fwd_kernel<float, S, true><<<grid, block, 0, st>>>(a, tl)
-             : gated_fwd_kernel<float, S, false><<<grid, block, 0, st>>>(a, tl);
-    else
-        a.cu ? gated_fwd_kernel<__bf16, S, true><<<grid, block, 0, st>>>(a, tl)
-             : gated_fwd_kernel<__bf16, S, false><<<grid, block, 0, st>>>(a, tl);
-    e = hipGetLastError();
-    if (e != hipSuccess || !a.x_codes) return e;
-    const long long rows = (long long)a.B * a.T;
-    e = launch_ckpt_pack(rows, a.D, dtype, a.x, a.x_stride, a.x_codes, a.x_scales, st);
-    if (e != hipSuccess) return e;
-    return launch_ckpt_pack(rows, a.D, dtype, a.g, a.g_stride, a.g_codes, a.g_scales, st);
+    if (a.T > 0)
+        return SSD_GATED_RUN(run_fwd, fwd_vec);
+    if (!a.final_state) return hipSuccess;
+    const long long n = (long long)(a.cu ? a.nseq : a.B) * a.D;
+    gated_carry_kernel<<<blocks_of(n), kThreads, 0, st>>>(a.init, a.final_state, n);
+    return hipGetLastError();
 }
 
 hipError_t launch_gated_bwd(ssd_dtype dtype, const GatedBwdArgs& a, void* ws, hipStream_t st) {
-    if (a.T == 0 || a.B == 0) {
-        const long long n = (long long)a.B * a.D;
-        if (a.d_init && n > 0)
-            gated_carry_kernel<<<blocks_of(n), kThreads, 0, st>>>(a.d_final, a.d_init, n);
-        if (a.d_bias)
-            gated_carry_kernel<<<blocks_of(a.D), kThreads, 0, st>>>(nullptr, a.d_bias, a.D);
-        return hipGetLastError();
-    }
-    const Layout l = layout(a.B, a.T, a.D, bwd_steps(dtype));
-    hipError_t e = prepare(l, (char*)ws, a.cu, a.nseq, a.T, a.D, nullptr, st);
-    if (e != hipSuccess) return e;
-    const Tiles tl = tiles_of(l, a.B, (char*)ws, a.cu != nullptr);
-    const dim3 grid((unsigned)l.tiles), block(kTileThreads);
-    const int rows = a.B * l.nk;
-    float* part = !a.d_bias ? nullptr : rows == 1 ? a.d_bias : (float*)((char*)ws + l.part);
-#define SSD_GATED_BWD(T, DT, PACKED, CODES) \
-    gated_bwd_kernel<T, bwd_steps(DT), PACKED, CODES><<<grid, block, 0, st>>>(a, tl, part)
-    const bool codes = a.x_codes != nullptr, packed = a.cu != nullptr;
-    if (dtype == SSD_F32) {
-        if (packed) codes ? SSD_GATED_BWD(float, SSD_F32, true, true) : SSD_GATED_BWD(float, SSD_F32, true, false);
-        else codes ? SSD_GATED_BWD(float, SSD_F32, false, true) : SSD_GATED_BWD(float, SSD_F32, false, false);
-    } else {
-        if (packed) codes ? SSD_GATED_BWD(__bf16, SSD_BF16, true, true) : SSD_GATED_BWD(__bf16, SSD_BF16, true, false);
-        else codes ? SSD_GATED_BWD(__bf16, SSD_BF16, false, true) : SSD_GATED_BWD(__bf16, SSD_BF16, false, false);
-    }
-#undef SSD_GATED_BWD
-    e = hipGetLastError();
-    if (e != hipSuccess || !a.d_bias || rows == 1) return e;
-    gated_dbias_kernel<<<(unsigned)l.blocks, 1024, 0, st>>>(part, a.d_bias, rows, a.D);
+    if (a.T > 0 && a.B > 0)
+        return SSD_GATED_RUN(run_bwd, bwd_vec);
+    const long long n = (long long)a.B * a.D;
+    if (a.d_init && n > 0)
+        gated_carry_kernel<<<blocks_of(n), kThreads, 0, st>>>(a.d_final, a.d_init, n);
+    if (a.d_bias)
+        gated_carry_kernel<<<blocks_of(a.D), kThreads, 0, st>>>(nullptr, a.d_bias, a.D);
     return hipGetLastError();
 }
 

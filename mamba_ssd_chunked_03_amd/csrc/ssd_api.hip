@@ -797,9 +797,12 @@ ssd_status gated_check(const ssd_gated_dims* d) {
     return SSD_OK;
 }
 
-// x, g, dh, dx, dg: rows of D values with this stride
+// x, g, dh, dx, dg: rows of D values with this stride; the rows of a kernel's tile (at most
+// 256 steps) lie within 2^31 bytes
 bool gated_stride(const ssd_gated_dims* d, int64_t stride) {
-    return stride >= d->channels && below({d->batch, d->seqlen, stride}, kFar);
+    const int64_t steps = d->seqlen < 256 ? d->seqlen : 256;
+    return stride >= d->channels && below({d->batch, d->seqlen, stride}, kFar) &&
+           (steps <= 1 || below({steps, stride}, (int64_t)1 << 29));
 }
 
 // packed rows: one batch element, at least one sequence, no states from outside

@@ -51,6 +51,9 @@ def test_forward_refusals(lib):
     assert fwd(lib, gdims(b=1 << 62, t=4)) == DIMS
     assert fwd(lib, xs=63) == DIMS and fwd(lib, gs=63) == DIMS
     assert fwd(lib, xs=1 << 62) == DIMS and fwd(lib, gs=-1) == DIMS
+    assert fwd(lib, gdims(t=300), xs=1 << 21) == DIMS and fwd(lib, gs=1 << 23) == DIMS
+    assert fwd(lib, gdims(t=300), xs=(1 << 21) - 1, h=None) == NULL  # the stride is taken
+    assert fwd(lib, gdims(t=1), xs=1 << 40, h=None) == NULL
     assert fwd(lib, dtype=2) == UNSUPPORTED and fwd(lib, dtype=-1) == UNSUPPORTED
     assert lib.ssd_gated_fwd(None, 1, P, 64, P, 64, P, None, 0, None, P, P, None, P, 1 << 40,
                              None) == NULL
