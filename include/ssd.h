@@ -542,7 +542,7 @@ ssd_status ssd_gated_bwd_ckpt(const ssd_gated_dims* dims, ssd_dtype dtype, const
  *   x, g    rows of D values in `dtype` at x_stride, g_stride elements (>= D)
  *   state   [B][D] fp32, read and updated in place (ssd_gated_fwd's final_state continues
  *           here);  h [B][D] in `dtype`
- * Alignment as above; no workspace.  Errors as ssd_fwd. */
+ * B * ceil(D/4) < 2^31; alignment as above; no workspace.  Errors as ssd_fwd. */
 ssd_status ssd_gated_step(const ssd_gated_dims* dims, ssd_dtype dtype, const void* x,
                           int64_t x_stride, const void* g, int64_t g_stride, const float* bias,
                           float* state, void* h, void* stream);

@@ -6,7 +6,6 @@ HIP stream go to the C ABI.  Every step of the computation runs in libssd's kern
 there is no fallback of any kind: if libssd.so is missing the first call raises.
 """
 import ctypes
-import functools
 import os
 
 import torch
@@ -796,34 +795,46 @@ def ssd_fwd_varlen(x, dt, A, B, C, D, chunk_len, cu_seqlens, y=None, final_state
 
 
 # ---------------------------------------------------------------- 8-bit activation checkpoints
-def _on_stream(call):
-    """Run a binding call with its `stream` argument (when given) as torch's current stream,
-    so that outputs and workspaces allocated inside belong to the stream that uses them."""
-    @functools.wraps(call)
-    def wrapped(*args, stream=None, **kw):
-        if stream is None:
-            return call(*args, **kw)
-        with torch.cuda.stream(stream):
-            return call(*args, stream=stream, **kw)
-    return wrapped
-
-
-def _launch(fn, dev, stream, *args):
-    """fn(*args, stream) on dev's current stream with dev the current device."""
-    if dev.type != "cuda":
-        raise ValueError(f"tensors must be on a GPU, got {dev}")
-    if stream is not None and stream.device != dev:
+def _on(stream, dev, call, *args):
+    """call(*args) with `stream` as torch's current stream, so that outputs and workspaces
+    allocated inside belong to the stream that uses them."""
+    if stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors on {dev}")
-    st = torch.cuda.current_stream(dev).cuda_stream
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, st))
+    with torch.cuda.stream(stream):
+        return call(*args)
+
+
+def _launch(fn, dev, *args):
+    """fn(*args, stream) on dev's current stream, with dev the current device."""
+    index = dev.index
+    if dev.type != "cuda" or index is None:
+        raise ValueError(f"tensors must be on a GPU, got {dev}")
+    if index == torch.cuda.current_device():
+        code = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, st))
+            code = fn(*args, _raw_stream(index))
+    if code != 0:
+        _check(code)
+
+
+# the current stream's handle; torch.cuda.current_stream builds a Stream object around it
+# first, which takes 2 us of the 6 that a small call spends in this module
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
+
+
+def _flat(t, name, dtype, dev, shape):
+    """The address of a contiguous tensor with exactly this dtype, device and shape."""
+    if t is not None and t.dtype is dtype and t.device == dev and t.shape == shape \
+            and t.is_contiguous():
+        return t.data_ptr()
+    _shape(_need(t, name, dtype, dev), name, shape)
+    return t.data_ptr()
 
 
 def _rows(t, name, dtype=None, device=None):
@@ -832,24 +843,27 @@ def _rows(t, name, dtype=None, device=None):
     wider tensor is fine)."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if dtype is not None and t.dtype != dtype:
+    if dtype is not None and t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    shape, width = t.shape, t.shape[-1]
+    shape = t.shape
+    width = shape[-1]
     if t.is_contiguous() or t.numel() == 0:
         return width
-    if width > 1 and t.stride(-1) != 1:
+    strides = t.stride()
+    if width > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must have contiguous rows")
     stride, span = width, None  # span: what the next leading dimension's stride has to be
-    for k in range(t.dim() - 2, -1, -1):
-        if shape[k] == 1:
+    for k in range(len(shape) - 2, -1, -1):
+        n = shape[k]
+        if n == 1:
             continue
         if span is None:
-            stride = t.stride(k)
-        elif t.stride(k) != span:
+            stride = strides[k]
+        elif strides[k] != span:
             raise ValueError(f"{name}: rows must be evenly spaced")
-        span = t.stride(k) * shape[k]
+        span = strides[k] * n
     if stride < width:
         raise ValueError(f"{name}: rows overlap")
     return stride
@@ -877,12 +891,13 @@ def _row_count(shape):
     return n
 
 
-@_on_stream
 def ssd_ckpt_pack(src, codes=None, scales=None, stream=None):
     """codes, scales of src's rows (libssd.ssd_ckpt_pack).
 
     src [..., width] fp32 or bf16 with evenly spaced rows (a column range of a wider tensor
     is fine); codes int8 of src's shape and scales fp32 [..., ceil(width / 64)], contiguous."""
+    if stream is not None:
+        return _on(stream, src.device, ssd_ckpt_pack, src, codes, scales)
     if src.dim() < 1:
         raise ValueError("src must have at least one dimension")
     dev, shape = src.device, src.shape
@@ -890,28 +905,27 @@ def ssd_ckpt_pack(src, codes=None, scales=None, stream=None):
     sshape = shape[:-1] + (ckpt_groups(shape[-1]),)
     codes = torch.empty(shape, dtype=torch.int8, device=dev) if codes is None else codes
     scales = torch.empty(sshape, dtype=torch.float32, device=dev) if scales is None else scales
-    _out(codes, "codes", torch.int8, dev, shape)
-    _out(scales, "scales", torch.float32, dev, sshape)
-    _launch(library().ssd_ckpt_pack, dev, stream, _row_count(shape), shape[-1], code, _addr(src),
-            stride, _addr(codes), _addr(scales))
+    _launch(library().ssd_ckpt_pack, dev, _row_count(shape), shape[-1], code, src.data_ptr(),
+            stride, _flat(codes, "codes", torch.int8, dev, shape),
+            _flat(scales, "scales", torch.float32, dev, sshape))
     return codes, scales
 
 
-@_on_stream
 def ssd_ckpt_unpack(codes, scales, dtype=torch.bfloat16, out=None, stream=None):
     """The values that codes and scales stand for (libssd.ssd_ckpt_unpack), in dtype (fp32 or
     bf16); out may be a column range of a wider tensor."""
     dev, shape = codes.device, codes.shape
+    if stream is not None:
+        return _on(stream, dev, ssd_ckpt_unpack, codes, scales, dtype, out)
     if codes.dim() < 1:
         raise ValueError("codes must have at least one dimension")
-    _need(codes, "codes", torch.int8)
-    _shape(_need(scales, "scales", torch.float32, dev), "scales",
-           shape[:-1] + (ckpt_groups(shape[-1]),))
+    pc = _flat(codes, "codes", torch.int8, dev, shape)
+    ps = _flat(scales, "scales", torch.float32, dev, shape[:-1] + (ckpt_groups(shape[-1]),))
     out = torch.empty(shape, dtype=dtype, device=dev) if out is None else out
     code, stride = _code_of(out, "out"), _rows(out, "out", dtype, dev)
     _shape(out, "out", shape)
-    _launch(library().ssd_ckpt_unpack, dev, stream, _row_count(shape), shape[-1], code,
-            _addr(codes), _addr(scales), _addr(out), stride)
+    _launch(library().ssd_ckpt_unpack, dev, _row_count(shape), shape[-1], code, pc, ps,
+            out.data_ptr(), stride)
     return out
 
 
@@ -920,7 +934,6 @@ def ssd_bwd_ckpt_workspace_size(dims, dtype, chunk_len):
                                                      int(chunk_len)))
 
 
-@_on_stream
 def ssd_bwd_ckpt(x, dt, A, B, C, D, chunk_len, dy, ngroups, init_state=None, d_final=None,
                  want_d_init=True, out=None, workspace=None, stream=None):
     """ssd_bwd with x, B and C kept as 8-bit checkpoints (libssd.ssd_bwd_ckpt).
@@ -929,6 +942,9 @@ def ssd_bwd_ckpt(x, dt, A, B, C, D, chunk_len, dy, ngroups, init_state=None, d_f
     rows; dy [B,T,H,P] gives the sizes and the dtype of dx, dB and dC, ngroups G.  The other
     arguments and the returned dict are as for ssd_bwd."""
     f32, i8, dev = torch.float32, torch.int8, dy.device
+    if stream is not None:
+        return _on(stream, dev, ssd_bwd_ckpt, x, dt, A, B, C, D, chunk_len, dy, ngroups,
+                   init_state, d_final, want_d_init, out, workspace)
     code = _code_of(dy, "dy")
     _need(dy, "dy")
     if dy.dim() != 4 or int(ngroups) < 1:
@@ -963,7 +979,7 @@ def ssd_bwd_ckpt(x, dt, A, B, C, D, chunk_len, dy, ngroups, init_state=None, d_f
         ws = ssd_bwd_ckpt_workspace_size(d, dy.dtype, chunk_len)
         workspace = torch.empty(max(ws, 1), dtype=torch.uint8, device=dev)
     _need(workspace, "workspace", device=dev)
-    _launch(library().ssd_bwd_ckpt, dev, stream, ctypes.byref(d), code, _addr(x[0]), _addr(x[1]),
+    _launch(library().ssd_bwd_ckpt, dev, ctypes.byref(d), code, _addr(x[0]), _addr(x[1]),
             _addr(dt), _addr(A), _addr(B[0]), _addr(B[1]), _addr(C[0]), _addr(C[1]), _addr(D),
             int(chunk_len), _addr(init_state), _addr(dy), _addr(d_final), _addr(o["dx"]),
             _addr(o["ddt"]), _addr(o["dA"]), _addr(o["dB"]), _addr(o["dC"]), _addr(o["dD"]),
@@ -1006,25 +1022,25 @@ def _gated_saved(saved, dev, shape, codes):
     """saved's buffers checked against [B, T, channels]; codes: True (required), False (not
     passed on) or None (passed on where given)."""
     bz, T, D = shape
-    _shape(_need(saved.get("entry_states"), "entry_states", torch.float32, dev), "entry_states",
-           (bz, nchunks(T, GATED_CHUNK), D))
+    entry = _flat(saved.get("entry_states"), "entry_states", torch.float32, dev,
+                  (bz, nchunks(T, GATED_CHUNK), D))
     names = ("x_codes", "x_scales", "g_codes", "g_scales")
     if codes is None:
         codes = any(saved.get(n) is not None for n in names)
     if not codes:
-        return SsdGatedSaved(_addr(saved["entry_states"]), None, None, None, None)
-    for n in names:
-        last, dty = (D, torch.int8) if n.endswith("codes") else (ckpt_groups(D), torch.float32)
-        _shape(_need(saved.get(n), n, dty, dev), n, (bz, T, last))
-    return SsdGatedSaved(_addr(saved["entry_states"]), *(_addr(saved[n]) for n in names))
+        return SsdGatedSaved(entry, None, None, None, None)
+    kinds = ((torch.int8, shape), (torch.float32, (bz, T, ckpt_groups(D)))) * 2
+    return SsdGatedSaved(entry, *(_flat(saved.get(n), n, dty, dev, kshape)
+                                  for n, (dty, kshape) in zip(names, kinds)))
 
 
 def _gated_common(dims, dev, bias, cu_seqlens, check):
-    """(number of sequences, rows of a final state) with bias and cu_seqlens checked."""
+    """(address of bias, number of sequences, rows of a final state), bias and cu_seqlens
+    checked."""
     if bias is not None:
-        _shape(_need(bias, "bias", torch.float32, dev), "bias", (dims.channels,))
+        bias = _flat(bias, "bias", torch.float32, dev, (dims.channels,))
     if cu_seqlens is None:
-        return 0, dims.batch
+        return bias, 0, dims.batch
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be [nseq + 1] with nseq >= 1")
@@ -1034,7 +1050,8 @@ def _gated_common(dims, dev, bias, cu_seqlens, check):
         cu = cu_seqlens.cpu()
         if int(cu[0]) != 0 or int(cu[-1]) != dims.seqlen or bool((cu[1:] < cu[:-1]).any()):
             raise ValueError(f"cu_seqlens must rise from 0 to T = {dims.seqlen}")
-    return cu_seqlens.numel() - 1, cu_seqlens.numel() - 1
+    nseq = cu_seqlens.numel() - 1
+    return bias, nseq, nseq
 
 
 def _gated_workspace(workspace, dims, dev):
@@ -1044,7 +1061,6 @@ def _gated_workspace(workspace, dims, dev):
     return _need(workspace, "workspace", device=dev)
 
 
-@_on_stream
 def ssd_gated_fwd(x, g, bias=None, init_state=None, cu_seqlens=None, saved=None, h=None,
                   final_state=None, want_final=True, workspace=None, check_cu_seqlens=True,
                   stream=None):
@@ -1055,35 +1071,40 @@ def ssd_gated_fwd(x, g, bias=None, init_state=None, cu_seqlens=None, saved=None,
     buffers of ssd_gated_saved(x), filled for the backward.  cu_seqlens int32 [nseq + 1] on
     the device: a packed row (B = 1), final_state [nseq, channels]; it is copied to the host
     and checked unless check_cu_seqlens is False (which waits for the stream)."""
-    dims, dev, f32 = _gated_dims(x), x.device, torch.float32
-    code = _code_of(x, "x")
-    xs, gs = _rows(x, "x"), _rows(g, "g", x.dtype, dev)
-    _shape(g, "g", x.shape)
-    nseq, ends = _gated_common(dims, dev, bias, cu_seqlens, check_cu_seqlens)
+    dims, dev, f32, shape = _gated_dims(x), x.device, torch.float32, x.shape
+    if stream is not None:
+        return _on(stream, dev, ssd_gated_fwd, x, g, bias, init_state, cu_seqlens, saved, h,
+                   final_state, want_final, workspace, check_cu_seqlens)
+    code, dtype = _code_of(x, "x"), x.dtype
+    xs, gs = _rows(x, "x"), _rows(g, "g", dtype, dev)
+    _shape(g, "g", shape)
+    pb, nseq, ends = _gated_common(dims, dev, bias, cu_seqlens, check_cu_seqlens)
+    pi = pf = sv = None
     if init_state is not None:
-        _shape(_need(init_state, "init_state", f32, dev), "init_state", (x.shape[0], x.shape[2]))
-    h = torch.empty(x.shape, dtype=x.dtype, device=dev) if h is None else h
-    _out(h, "h", x.dtype, dev, x.shape)
-    fshape = (ends, x.shape[2])
+        pi = _flat(init_state, "init_state", f32, dev, (shape[0], shape[2]))
+    h = torch.empty(shape, dtype=dtype, device=dev) if h is None else h
     if final_state is None and want_final:
-        final_state = torch.empty(fshape, dtype=f32, device=dev)
-    _out(final_state, "final_state", f32, dev, fshape)
-    sv = None if saved is None else ctypes.byref(_gated_saved(saved, dev, x.shape, None))
+        final_state = torch.empty((ends, shape[2]), dtype=f32, device=dev)
+    if final_state is not None:
+        pf = _flat(final_state, "final_state", f32, dev, (ends, shape[2]))
+    if saved is not None:
+        sv = ctypes.byref(_gated_saved(saved, dev, shape, None))
     workspace = _gated_workspace(workspace, dims, dev)
-    _launch(library().ssd_gated_fwd, dev, stream, ctypes.byref(dims), code, _addr(x), xs,
-            _addr(g), gs, _addr(bias), _addr(cu_seqlens), nseq, _addr(init_state), _addr(h),
-            _addr(final_state), sv, _addr(workspace), _nbytes(workspace))
+    _launch(library().ssd_gated_fwd, dev, ctypes.byref(dims), code, x.data_ptr(), xs,
+            g.data_ptr(), gs, pb, _addr(cu_seqlens), nseq, pi, _flat(h, "h", dtype, dev, shape),
+            pf, sv, workspace.data_ptr(), _nbytes(workspace))
     return h, final_state
 
 
 def _gated_bwd(fn, inputs, dims, shape, dtype, dev, bias, dh, saved, d_final, cu_seqlens,
-               want_d_bias, want_d_init, out, workspace, check, stream):
+               want_d_bias, want_d_init, out, workspace, check):
     f32 = torch.float32
     hs = _rows(dh, "dh", dtype, dev)
     _shape(dh, "dh", shape)
-    nseq, ends = _gated_common(dims, dev, bias, cu_seqlens, check)
+    pb, nseq, ends = _gated_common(dims, dev, bias, cu_seqlens, check)
+    pf = None
     if d_final is not None:
-        _shape(_need(d_final, "d_final", f32, dev), "d_final", (ends, dims.channels))
+        pf = _flat(d_final, "d_final", f32, dev, (ends, dims.channels))
     sv = _gated_saved(saved, dev, shape, not inputs)
     o = dict(out or {})
     for k in ("dx", "dg"):
@@ -1092,22 +1113,21 @@ def _gated_bwd(fn, inputs, dims, shape, dtype, dev, bias, dh, saved, d_final, cu
         _shape(o[k], k, shape)
     strides = [_rows(o[k], k, dtype, dev) for k in ("dx", "dg")]
     want_d_init = want_d_init and cu_seqlens is None
+    sums = []
     for k, want, kshape in (("d_bias", want_d_bias, (dims.channels,)),
                             ("d_init", want_d_init, (dims.batch, dims.channels))):
         if not want:
             o[k] = None
         elif o.get(k) is None:
             o[k] = torch.empty(kshape, dtype=f32, device=dev)
-        _out(o[k], k, f32, dev, kshape)
+        sums.append(_flat(o[k], k, f32, dev, kshape) if want else None)
     workspace = _gated_workspace(workspace, dims, dev)
-    _launch(fn, dev, stream, ctypes.byref(dims), _DTYPE_CODE[dtype], *inputs, _addr(bias),
-            _addr(cu_seqlens), nseq, ctypes.byref(sv), _addr(dh), hs, _addr(d_final),
-            _addr(o["dx"]), strides[0], _addr(o["dg"]), strides[1], _addr(o["d_bias"]),
-            _addr(o["d_init"]), _addr(workspace), _nbytes(workspace))
+    _launch(fn, dev, ctypes.byref(dims), _DTYPE_CODE[dtype], *inputs, pb, _addr(cu_seqlens), nseq,
+            ctypes.byref(sv), dh.data_ptr(), hs, pf, o["dx"].data_ptr(), strides[0],
+            o["dg"].data_ptr(), strides[1], *sums, workspace.data_ptr(), _nbytes(workspace))
     return o
 
 
-@_on_stream
 def ssd_gated_bwd(x, g, bias, dh, saved, d_final=None, cu_seqlens=None, want_d_bias=True,
                   want_d_init=True, out=None, workspace=None, check_cu_seqlens=True,
                   stream=None):
@@ -1117,43 +1137,46 @@ def ssd_gated_bwd(x, g, bias, dh, saved, d_final=None, cu_seqlens=None, want_d_b
     row).  out may hold preallocated tensors under those names; dx and dg may be column
     ranges of one gradient of the projection's output."""
     dims, dev = _gated_dims(x), x.device
+    if stream is not None:
+        return _on(stream, dev, ssd_gated_bwd, x, g, bias, dh, saved, d_final, cu_seqlens,
+                   want_d_bias, want_d_init, out, workspace, check_cu_seqlens)
     _code_of(x, "x")
     xs, gs = _rows(x, "x"), _rows(g, "g", x.dtype, dev)
     _shape(g, "g", x.shape)
-    return _gated_bwd(library().ssd_gated_bwd, (_addr(x), xs, _addr(g), gs), dims, x.shape,
-                      x.dtype, dev, bias, dh, saved, d_final, cu_seqlens, want_d_bias,
-                      want_d_init, out, workspace, check_cu_seqlens, stream)
+    return _gated_bwd(library().ssd_gated_bwd, (x.data_ptr(), xs, g.data_ptr(), gs), dims,
+                      x.shape, x.dtype, dev, bias, dh, saved, d_final, cu_seqlens, want_d_bias,
+                      want_d_init, out, workspace, check_cu_seqlens)
 
 
-@_on_stream
 def ssd_gated_bwd_ckpt(bias, dh, saved, d_final=None, cu_seqlens=None, want_d_bias=True,
                        want_d_init=True, out=None, workspace=None, check_cu_seqlens=True,
                        stream=None):
     """ssd_gated_bwd from the 8-bit checkpoints of x and g in saved (libssd.ssd_gated_bwd_ckpt:
     ssd_gated_saved(x, ckpt=True), filled by ssd_gated_fwd)."""
     dims = _gated_dims(dh, "dh")
+    if stream is not None:
+        return _on(stream, dh.device, ssd_gated_bwd_ckpt, bias, dh, saved, d_final, cu_seqlens,
+                   want_d_bias, want_d_init, out, workspace, check_cu_seqlens)
     _code_of(dh, "dh")
     return _gated_bwd(library().ssd_gated_bwd_ckpt, (), dims, dh.shape, dh.dtype, dh.device, bias,
                       dh, saved, d_final, cu_seqlens, want_d_bias, want_d_init, out, workspace,
-                      check_cu_seqlens, stream)
+                      check_cu_seqlens)
 
 
-@_on_stream
 def ssd_gated_step(x, g, bias, state, h=None, stream=None):
     """One step of the gated recurrence (libssd.ssd_gated_step): x, g [batch, channels] (rows
     may be column ranges), state [batch, channels] fp32 (updated in place).  Returns h in
     x's dtype."""
     if x.dim() != 2:
         raise ValueError(f"x must be [batch, channels], got {tuple(x.shape)}")
-    dev, shape = x.device, x.shape
-    code, xs, gs = _code_of(x, "x"), _rows(x, "x"), _rows(g, "g", x.dtype, dev)
+    dev, shape, dtype, f32 = x.device, x.shape, x.dtype, torch.float32
+    if stream is not None:
+        return _on(stream, dev, ssd_gated_step, x, g, bias, state, h)
+    code, xs, gs = _code_of(x, "x"), _rows(x, "x"), _rows(g, "g", dtype, dev)
     _shape(g, "g", shape)
-    if bias is not None:
-        _shape(_need(bias, "bias", torch.float32, dev), "bias", (shape[1],))
-    _shape(_need(state, "state", torch.float32, dev), "state", shape)
-    h = torch.empty(shape, dtype=x.dtype, device=dev) if h is None else h
-    _out(h, "h", x.dtype, dev, shape)
-    dims = SsdGatedDims(shape[0], 1, shape[1])
-    _launch(library().ssd_gated_step, dev, stream, ctypes.byref(dims), code, _addr(x), xs,
-            _addr(g), gs, _addr(bias), _addr(state), _addr(h))
+    h = torch.empty(shape, dtype=dtype, device=dev) if h is None else h
+    _launch(library().ssd_gated_step, dev, ctypes.byref(SsdGatedDims(shape[0], 1, shape[1])), code,
+            x.data_ptr(), xs, g.data_ptr(), gs,
+            None if bias is None else _flat(bias, "bias", f32, dev, (shape[1],)),
+            _flat(state, "state", f32, dev, shape), _flat(h, "h", dtype, dev, shape))
     return h

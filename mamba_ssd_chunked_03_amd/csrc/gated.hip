@@ -40,11 +40,11 @@ constexpr int kLanes = 16;     // lanes along a row of a tile
 #endif
 constexpr int kFwdRuns = X_FR, kBwdRuns = X_BR;      // runs of a tile
 #ifndef X_LOOK
-#define X_LOOK 8
+#define X_LOOK 4
 #endif
 constexpr int kLook = X_LOOK;       // spans looked at together
 #ifndef X_SCAN
-#define X_SCAN 8
+#define X_SCAN 4
 #endif
 constexpr int kScan = X_SCAN;       // runs scanned together
 #ifndef X_FV
@@ -53,12 +53,16 @@ constexpr int kScan = X_SCAN;       // runs scanned together
 #endif
 #ifndef X_BV
 #define X_BV 4
-#define X_BS 4
+#define X_BS 8
 #endif
 constexpr int fwd_vec(ssd_dtype t) { return t == SSD_F32 ? 4 : X_FV; }
 constexpr int bwd_vec(ssd_dtype t) { return t == SSD_F32 ? 4 : X_BV; }
-constexpr int fwd_steps(ssd_dtype t) { return t == SSD_F32 ? 8 : X_FS; }
-constexpr int bwd_steps(ssd_dtype t) { return t == SSD_F32 ? 4 : X_BS; }
+#ifndef X_FS32
+#define X_FS32 8
+#define X_BS32 4
+#endif
+constexpr int fwd_steps(ssd_dtype t) { return t == SSD_F32 ? X_FS32 : X_FS; }
+constexpr int bwd_steps(ssd_dtype t) { return t == SSD_F32 ? X_BS32 : X_BS; }
 
 // ---- pieces: a lane's V neighbouring channels of a row -------------------------------------
 // Rows need only element alignment, so pieces are loaded and stored as unaligned vectors (one
@@ -85,6 +89,11 @@ template <typename T, int V> struct Piece {
     __device__ __forceinline__ void load(const T* p) {
         const Words<W> b =
             __builtin_nontemporal_load((const typename AnyWords<T, W>::Any*)p);
+#pragma unroll
+        for (int i = 0; i < W; ++i) w[i] = b[i];
+    }
+    __device__ __forceinline__ void load_cached(const T* p) {
+        const Words<W> b = *(const typename AnyWords<T, W>::Any*)p;
 #pragma unroll
         for (int i = 0; i < W; ++i) w[i] = b[i];
     }
@@ -123,14 +132,15 @@ template <int V, bool NARROW> __device__ __forceinline__ Own own_of(int piece, i
     return Own{min(c, D - V), n >= V ? 0 : n > 0 ? V - n : V, V};
 }
 
-template <typename T, int V>
+template <typename T, int V, bool CACHED = false>
 __device__ __forceinline__ void store(T* p, const float (&v)[V], const Own& o) {
     constexpr int W = V * (int)sizeof(T) / 4;
     union { T t[V]; Words<W> b; } u;
 #pragma unroll
     for (int i = 0; i < V; ++i) u.t[i] = from_f32<T>(v[i]);
     if (o.hi - o.lo == V) {
-        __builtin_nontemporal_store(u.b, (typename AnyWords<T, W>::Any*)p);
+        if (CACHED) *(typename AnyWords<T, W>::Any*)p = u.b;
+        else __builtin_nontemporal_store(u.b, (typename AnyWords<T, W>::Any*)p);
     } else {
 #pragma unroll
         for (int i = 0; i < V; ++i)
@@ -575,6 +585,15 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_fwd_kernel(GatedFwdArg
 }
 
 // ---- backward -----------------------------------------------------------------------------
+// the sum over the four rows of 16 lanes of a wave, in all of them
+__device__ __forceinline__ float row_sum(float v) {
+    unsigned u = __float_as_uint(v);
+    auto p = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+    u = __float_as_uint(__uint_as_float(p[0]) + __uint_as_float(p[1]));
+    p = __builtin_amdgcn_permlane32_swap(u, u, false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
 // x and g of a run, from rows in T or from 8-bit codes and their scales.
 template <typename T, int V, int S, bool CODES, bool NARROW> struct RunIn;
 template <typename T, int V, int S, bool NARROW> struct RunIn<T, V, S, false, NARROW> {
@@ -624,8 +643,10 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
                                                                      float* part) {
     constexpr int C = kLanes * V, kTile = RUNS * S;
     constexpr int kChunkRuns = kGatedChunk / S;
-    static_assert(kTile % kGatedChunk == 0 && RUNS * kLanes >= 2 * C, "tiles hold whole chunks");
+    static_assert(kTile % kGatedChunk == 0 && RUNS * kLanes >= 3 * C, "tiles hold whole chunks");
+    constexpr int kWaves = RUNS * kLanes / 64;
     __shared__ __align__(16) float sP[RUNS * C], sH[RUNS * C], sC[RUNS * C], sR[RUNS * C], sE[C];
+    __shared__ __align__(16) float sD[kWaves * C];  // d_bias' share of every wave
     __shared__ unsigned sNext, sCut[RUNS];
     const Group group = group_of(tl);
     unsigned t = first_number(tl, group, &sNext);
@@ -645,6 +666,16 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
         x.load(a.x, a.x_stride, a.x_codes, a.x_scales, row0, rows, w, a.D);
         load_run<T, V, S, NARROW>(dh, (const T*)a.dh + row0 * a.dh_stride, a.dh_stride, w.r, rows,
                                   w.o);
+    };
+    Place before;  // the tile whose shares of d_bias are in sD
+    before.k = -1;
+    auto sum_up = [&](int col) {
+        bool owned;
+        const int c = channel_of<V, NARROW>(before.cb, col, a.D, &owned);
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < kWaves; ++i) s += sD[i * C + col];
+        if (owned) part[((long long)before.b * tl.nk + tl.nk - 1 - before.k) * a.D + c] = s;
     };
     fetch();
     for (;;) {
@@ -681,30 +712,32 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
                 w.o);
         };
         {
-            float P[V], H[V], G[V], q[S][V];
+            // G's carry out of the run in the same sweep: dh_j reaches it through the product
+            // of a up to j
+            float P[V], H[V], G[V];
+            bool cut = false;
 #pragma unroll
             for (int i = 0; i < V; ++i) P[i] = 1.f, H[i] = G[i] = 0.f;
 #pragma unroll
             for (int j = 0; j < S; ++j) {
                 if (PACKED && (starts >> j & 1)) {
+                    cut = true;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) P[i] = H[i] = 0.f;
+                    for (int i = 0; i < V; ++i) H[i] = 0.f;
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
-                    q[j][i] = gate_q(fmaf(g.get(j, i), kLog2e, bias[i]));
-                    if (!whole && ts + j >= a.T) q[j][i] = 0.f;
-                    H[i] = gate_step(q[j][i], x.get(j, i), H[i]);
-                    P[i] = fmaf(-q[j][i], P[i], P[i]);
+                    float q = gate_q(fmaf(g.get(j, i), kLog2e, bias[i]));
+                    if (!whole && ts + j >= a.T) q = 0.f;
+                    H[i] = gate_step(q, x.get(j, i), H[i]);
+                    P[i] = fmaf(-q, P[i], P[i]);
+                    if (!cut) G[i] = fmaf(P[i], dh[j].get(i), G[i]);
                 }
-            }
+                if (PACKED && !cut && (ends >> j & 1)) {
+                    float v[V];
+                    ending(j, v);
 #pragma unroll
-            for (int j = S - 1; j >= 0; --j) {
-                if (PACKED && (ends >> j & 1)) ending(j, G);
-#pragma unroll
-                for (int i = 0; i < V; ++i) {
-                    const float v = dh[j].get(i) + G[i];
-                    G[i] = PACKED && (starts >> j & 1) ? 0.f : fmaf(-q[j][i], v, v);
+                    for (int i = 0; i < V; ++i) G[i] = fmaf(P[i], v[i], G[i]);
                 }
             }
             put<V>(&sP[w.r * C], w.cq, P);
@@ -766,6 +799,8 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
                     e = PACKED && (cuts >> r & 1) ? v : fmaf(p, e, v);
                 }
             }
+        } else if (threadIdx.x < 3 * C) {
+            if (part && before.k >= 0) sum_up(threadIdx.x - 2 * C);
         }
         __syncthreads();
         float h[V], G[V], db[V];
@@ -827,29 +862,26 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
         }
         if (!PACKED && a.d_init && ts == 0)
             store<float, V>(a.d_init + (long long)w.b * a.D + w.o.c0, G, w.o);
-        const Place done = w;
-        t = next;
-        const bool more = t < group.tiles;
-        if (more) fetch();
-        if (part) {
-            put<V>(&sP[done.r * C], done.cq, db);  // the scans are done with sP
-            __syncthreads();
-            if (threadIdx.x < C) {
-                bool owned;
-                const int c = channel_of<V, NARROW>(done.cb, threadIdx.x, a.D, &owned);
-                float s = 0.f;
+        if (part) {  // the wave's four runs; summed up during the next tile's scan
 #pragma unroll
-                for (int r = 0; r < RUNS; ++r) s += sP[r * C + threadIdx.x];
-                if (owned) part[((long long)done.b * tl.nk + kt) * a.D + c] = s;
-            }
+            for (int i = 0; i < V; ++i) db[i] = row_sum(db[i]);
+            if (threadIdx.x % 64 < kLanes) put<V>(&sD[threadIdx.x / 64 * C], w.cq, db);
+            before = w;
         }
-        if (!more) break;
+        t = next;
+        if (t >= group.tiles) break;
+        fetch();
         __syncthreads();  // LDS is free again
+    }
+    if (part) {
+        __syncthreads();
+        if (threadIdx.x < C) sum_up(threadIdx.x);
     }
 }
 
 // ---- small kernels ------------------------------------------------------------------------
 constexpr int kThreads = 256;
+constexpr int kStepVec = 4;
 
 // Before a pass: the counters cleared, spans and carries marked missing, the start bits of a packed row, and zero
 // final states for its empty sequences.
@@ -898,6 +930,7 @@ __global__ __launch_bounds__(1024) void gated_dbias_kernel(const float* part, fl
     const int c = blockIdx.x * 64 + lane;
     float v = 0.f;
     if (c < D)
+#pragma unroll 8
         for (int r = w; r < rows; r += 16) v += part[(long long)r * D + c];
     s[w][lane] = v;
     __syncthreads();
@@ -912,17 +945,35 @@ __global__ __launch_bounds__(kThreads) void gated_carry_kernel(const float* src,
     if (id < n) dst[id] = src ? src[id] : 0.f;
 }
 
-template <typename T>
-__global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedStepArgs a) {
-    const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
-    if (id >= (long long)a.B * a.D) return;
-    const long long b = id / a.D;
-    const int d = (int)(id % a.D);
-    const float q = gate_q(fmaf(to_f32(((const T*)a.g)[b * a.g_stride + d]), kLog2e,
-                                (a.bias ? a.bias[d] : 0.f) * kLog2e));
-    const float h = gate_step(q, to_f32(((const T*)a.x)[b * a.x_stride + d]), a.state[id]);
-    a.state[id] = h;
-    ((T*)a.h)[id] = from_f32<T>(h);
+// One thread per piece of four channels of a row.  Cached accesses: the state comes back at
+// the next step.
+template <typename T, bool NARROW>
+__global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedStepArgs a, unsigned pieces) {
+    constexpr int V = kStepVec;
+    const unsigned id = blockIdx.x * kThreads + threadIdx.x;
+    const unsigned b = id / pieces;
+    if (b >= (unsigned)a.B) return;
+    const Own o = own_of<V, NARROW>(id % pieces, a.D);
+    const T* xp = (const T*)a.x + b * a.x_stride + o.c0;
+    const T* gp = (const T*)a.g + b * a.g_stride + o.c0;
+    float* sp = a.state + (long long)b * a.D + o.c0;
+    T* hp = (T*)a.h + (long long)b * a.D + o.c0;
+    Piece<T, V> x, g;
+    if (NARROW) {
+        x.load_part(xp, o.hi);
+        g.load_part(gp, o.hi);
+    } else {
+        x.load_cached(xp);
+        g.load_cached(gp);
+    }
+    float bias[V], s[V];
+    load_f32<V, NARROW>(bias, a.bias ? a.bias + o.c0 : nullptr, o);
+    load_f32<V, NARROW>(s, sp, o);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+        s[i] = gate_step(gate_q(fmaf(g.get(i), kLog2e, bias[i] * kLog2e)), x.get(i), s[i]);
+    store<float, V, true>(sp, s, o);
+    store<T, V, true>(hp, s, o);
 }
 
 unsigned blocks_of(long long n) { return (unsigned)((n + kThreads - 1) / kThreads); }
@@ -1087,11 +1138,15 @@ hipError_t launch_gated_bwd(ssd_dtype dtype, const GatedBwdArgs& a, void* ws, hi
 }
 
 hipError_t launch_gated_step(ssd_dtype dtype, const GatedStepArgs& a, hipStream_t st) {
-    const unsigned blocks = blocks_of((long long)a.B * a.D);
+    const unsigned pieces = (a.D + kStepVec - 1) / kStepVec;
+    const unsigned blocks = blocks_of((long long)a.B * pieces);
+    const bool narrow = a.D < kStepVec;
     if (dtype == SSD_F32)
-        gated_step_kernel<float><<<blocks, kThreads, 0, st>>>(a);
+        narrow ? gated_step_kernel<float, true><<<blocks, kThreads, 0, st>>>(a, pieces)
+               : gated_step_kernel<float, false><<<blocks, kThreads, 0, st>>>(a, pieces);
     else
-        gated_step_kernel<__bf16><<<blocks, kThreads, 0, st>>>(a);
+        narrow ? gated_step_kernel<__bf16, true><<<blocks, kThreads, 0, st>>>(a, pieces)
+               : gated_step_kernel<__bf16, false><<<blocks, kThreads, 0, st>>>(a, pieces);
     return hipGetLastError();
 }
 

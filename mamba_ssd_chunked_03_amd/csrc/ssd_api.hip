@@ -1033,7 +1033,9 @@ ssd_status ssd_gated_step(const ssd_gated_dims* dims, ssd_dtype dtype, const voi
     const ssd_status r = gated_check(&one);
     if (r != SSD_OK) return r;
     if (!valid_dtype(dtype)) return SSD_ERR_UNSUPPORTED;
-    if (!gated_stride(&one, x_stride) || !gated_stride(&one, g_stride)) return SSD_ERR_DIMS;
+    if (!gated_stride(&one, x_stride) || !gated_stride(&one, g_stride) ||
+        !below({one.batch, (one.channels + 3) / 4}, kMaxElems))
+        return SSD_ERR_DIMS;
     if (one.batch == 0 || one.channels == 0) return SSD_OK;
     if (!x || !g || !state || !h) return SSD_ERR_NULL;
     if (misaligned_elem({x, g, h}, dtype) || any_misaligned4({bias, state})) return SSD_ERR_ALIGN;

@@ -106,6 +106,7 @@ def test_step_refusals(lib):
         return lib.ssd_gated_step(dims or gdims(), dtype, x, xs, g, gs, bias, state, h, None)
     assert step(gdims(b=-1)) == DIMS and step(xs=63) == DIMS and step(gs=0) == DIMS
     assert step(dtype=3) == UNSUPPORTED
+    assert step(gdims(b=1 << 15, d=1 << 18), xs=1 << 18, gs=1 << 18) == DIMS
     for k in ("x", "g", "state", "h"):
         assert step(**{k: None}) == NULL
         assert step(**{k: 257}) == ALIGN
