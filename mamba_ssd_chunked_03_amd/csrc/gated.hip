@@ -31,38 +31,23 @@
 namespace ssd {
 namespace {
 
-constexpr int kLanes = 16;     // lanes along a row of a tile
-#ifndef X_FR
-#define X_FR 32
-#endif
-#ifndef X_BR
-#define X_BR 32
-#endif
-constexpr int kFwdRuns = X_FR, kBwdRuns = X_BR;      // runs of a tile
-#ifndef X_LOOK
-#define X_LOOK 4
-#endif
-constexpr int kLook = X_LOOK;       // spans looked at together
-#ifndef X_SCAN
-#define X_SCAN 4
-#endif
-constexpr int kScan = X_SCAN;       // runs scanned together
-#ifndef X_FV
-#define X_FV 8
-#define X_FS 4
-#endif
-#ifndef X_BV
-#define X_BV 4
-#define X_BS 8
-#endif
-constexpr int fwd_vec(ssd_dtype t) { return t == SSD_F32 ? 4 : X_FV; }
-constexpr int bwd_vec(ssd_dtype t) { return t == SSD_F32 ? 4 : X_BV; }
-#ifndef X_FS32
-#define X_FS32 8
-#define X_BS32 4
-#endif
-constexpr int fwd_steps(ssd_dtype t) { return t == SSD_F32 ? X_FS32 : X_FS; }
-constexpr int bwd_steps(ssd_dtype t) { return t == SSD_F32 ? X_BS32 : X_BS; }
+constexpr int kLanes = 16;  // lanes along a row of a tile
+constexpr int kRuns = 32;   // runs of a tile: 512 threads, two workgroups to a CU
+constexpr int kLook = 8;    // published spans looked at together
+constexpr int kScan = 8;    // runs that a scan reads together
+
+// V channels by S steps of a lane.  16 or 32 elements a lane in 16 or 8 byte pieces were
+// measured, at 4 x 4096 x 5120 (backward, and forward with codes at 8 x 2048 x 1536), at one
+// row of 65536 x 5120 (forward) and of 65536 x 256 (thin):
+//   bf16 forward  4 x 8: 100, 399, thin 37 us;    8 x 4: 100, 411, 40;   4 x 4: 105, 461, 51
+//   with codes    8 x 4: 118 us for the training pass;  4 x 8: 127: the 8-bit scales' two
+//                 divisions come once per step and lane
+//   bf16 backward 4 x 8: 183 us;  4 x 4: 189;  8 x 4: 228 (more registers than there are)
+//   fp32          4 x 8 forward, 4 x 4 backward: the same bytes a lane as in bf16
+constexpr int fwd_vec(ssd_dtype t, bool codes) { return t == SSD_BF16 && codes ? 8 : 4; }
+constexpr int fwd_steps(ssd_dtype t, bool codes) { return t == SSD_BF16 && codes ? 4 : 8; }
+constexpr int kBwdVec = 4;
+constexpr int bwd_steps(ssd_dtype t) { return t == SSD_BF16 ? 8 : 4; }
 
 // ---- pieces: a lane's V neighbouring channels of a row -------------------------------------
 // Rows need only element alignment, so pieces are loaded and stored as unaligned vectors (one
@@ -191,7 +176,9 @@ __device__ __forceinline__ int channel_of(int cb, int col, int D, bool* owned) {
 // ---- tiles, and the carry between them ----------------------------------------------------
 constexpr int kBlockTiles = 16;  // tiles of a block of a chain, and blocks of a larger one
 // Counters of tiles taken, each for a range of neighbouring chains and on a cache line of its
-// own; one counter alone where there are too few chains to share them out evenly.
+// own.  A counter serves one workgroup in about 9 ns: with one for all, the 512 workgroups
+// that start together wait 5 us for their first number (8 x 1024 x 1536 in bf16: forward 29
+// us, 22 with eight counters; backward 48 and 35).
 constexpr unsigned kCounters = 8, kCounterWords = 64;
 
 struct Tiles {
@@ -427,12 +414,20 @@ __device__ __forceinline__ void pack_run(const Piece<T, V> (&v)[S], int8_t* code
     }
 }
 
+// threadIdx.x, computed anew in every iteration: the addresses that follow from it would
+// otherwise be kept over the whole loop, in more registers than there are.
+__device__ __forceinline__ int fresh_thread() {
+    int t = threadIdx.x;
+    asm volatile("" : "+v"(t));
+    return t;
+}
+
 // ---- forward ------------------------------------------------------------------------------
-template <typename T, int V, int S, int RUNS, bool PACKED, bool CODES, bool NARROW>
-__global__ __launch_bounds__(RUNS * kLanes, 4) void gated_fwd_kernel(GatedFwdArgs a, Tiles tl) {
-    constexpr int C = kLanes * V, kTile = RUNS * S;
-    __shared__ __align__(16) float sP[RUNS * C], sH[RUNS * C], sE[C];
-    __shared__ unsigned sNext, sCut[RUNS];
+template <typename T, int V, int S, bool PACKED, bool CODES, bool NARROW>
+__global__ __launch_bounds__(kRuns * kLanes, 4) void gated_fwd_kernel(GatedFwdArgs a, Tiles tl) {
+    constexpr int C = kLanes * V, kTile = kRuns * S;
+    __shared__ __align__(16) float sP[kRuns * C], sH[kRuns * C], sE[C];
+    __shared__ unsigned sNext, sCut[kRuns];
     const Group group = group_of(tl);
     unsigned t = first_number(tl, group, &sNext);
     if (t >= group.tiles) return;
@@ -453,6 +448,7 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_fwd_kernel(GatedFwdArg
     };
     fetch();
     for (;;) {
+        const int tid = fresh_thread();
         const int t0 = w.k * kTile, ts = t0 + w.r * S;
         const int rows = min(kTile, a.T - t0);
         const bool whole = rows == kTile;
@@ -502,17 +498,17 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_fwd_kernel(GatedFwdArg
             put<V>(&sP[w.r * C], w.cq, P);
             put<V>(&sH[w.r * C], w.cq, H);
         }
-        if (threadIdx.x == 0) sNext = taken;
+        if (tid == 0) sNext = taken;
         __syncthreads();
         const unsigned next = __builtin_amdgcn_readfirstlane(sNext);
         unsigned cuts = 0;
         if (PACKED)
-            cuts = (unsigned)__ballot((threadIdx.x & 63) < RUNS && sCut[threadIdx.x % RUNS] != 0);
-        if (threadIdx.x < C) {
-            const int col = threadIdx.x;
+            cuts = (unsigned)__ballot((tid & 63) < kRuns && sCut[tid % kRuns] != 0);
+        if (tid < C) {
+            const int col = tid;
             float accP = 1.f, accH = 0.f;
 #pragma unroll
-            for (int r0 = 0; r0 < RUNS; r0 += kScan) {
+            for (int r0 = 0; r0 < kRuns; r0 += kScan) {
                 float p[kScan], h[kScan];
 #pragma unroll
                 for (int r = 0; r < kScan; ++r) {
@@ -539,7 +535,7 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_fwd_kernel(GatedFwdArg
             pack_run<T, V, S>(x, a.x_codes, a.x_scales, a, w, row0, rows);
         }
         __syncthreads();
-        if (CODES && threadIdx.x < C)
+        if (CODES && tid < C)
             pack_run<T, V, S>(x, a.x_codes, a.x_scales, a, w, row0, rows);
         float h[V];
         {
@@ -638,16 +634,16 @@ template <typename T, int V, int S, bool NARROW> struct RunIn<T, V, S, true, NAR
     }
 };
 
-template <typename T, int V, int S, int RUNS, bool PACKED, bool CODES, bool NARROW>
-__global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArgs a, Tiles tl,
+template <typename T, int V, int S, bool PACKED, bool CODES, bool NARROW>
+__global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdArgs a, Tiles tl,
                                                                      float* part) {
-    constexpr int C = kLanes * V, kTile = RUNS * S;
+    constexpr int C = kLanes * V, kTile = kRuns * S;
     constexpr int kChunkRuns = kGatedChunk / S;
-    static_assert(kTile % kGatedChunk == 0 && RUNS * kLanes >= 3 * C, "tiles hold whole chunks");
-    constexpr int kWaves = RUNS * kLanes / 64;
-    __shared__ __align__(16) float sP[RUNS * C], sH[RUNS * C], sC[RUNS * C], sR[RUNS * C], sE[C];
+    static_assert(kTile % kGatedChunk == 0 && kRuns * kLanes >= 3 * C, "tiles hold whole chunks");
+    constexpr int kWaves = kRuns * kLanes / 64;
+    __shared__ __align__(16) float sP[kRuns * C], sH[kRuns * C], sC[kRuns * C], sR[kRuns * C], sE[C];
     __shared__ __align__(16) float sD[kWaves * C];  // d_bias' share of every wave
-    __shared__ unsigned sNext, sCut[RUNS];
+    __shared__ unsigned sNext, sCut[kRuns];
     const Group group = group_of(tl);
     unsigned t = first_number(tl, group, &sNext);
     if (t >= group.tiles) return;
@@ -679,6 +675,7 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
     };
     fetch();
     for (;;) {
+        const int tid = fresh_thread();
         const int kt = tl.nk - 1 - w.k;
         const int t0 = kt * kTile, ts = t0 + w.r * S;
         const int rows = min(kTile, a.T - t0);
@@ -744,17 +741,17 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
             put<V>(&sH[w.r * C], w.cq, H);
             put<V>(&sC[w.r * C], w.cq, G);
         }
-        if (threadIdx.x == 0) sNext = taken;
+        if (tid == 0) sNext = taken;
         __syncthreads();
         const unsigned next = __builtin_amdgcn_readfirstlane(sNext);
         unsigned cuts = 0;
         if (PACKED)
-            cuts = (unsigned)__ballot((threadIdx.x & 63) < RUNS && sCut[threadIdx.x % RUNS] != 0);
-        if (threadIdx.x < C) {  // the first waves: G, last run first
-            const int col = threadIdx.x;
+            cuts = (unsigned)__ballot((tid & 63) < kRuns && sCut[tid % kRuns] != 0);
+        if (tid < C) {  // the first waves: G, last run first
+            const int col = tid;
             float accP = 1.f, accC = 0.f;
 #pragma unroll
-            for (int r0 = RUNS - kScan; r0 >= 0; r0 -= kScan) {
+            for (int r0 = kRuns - kScan; r0 >= 0; r0 -= kScan) {
                 float p[kScan], v[kScan];
 #pragma unroll
                 for (int r = 0; r < kScan; ++r) {
@@ -777,8 +774,8 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
                     ? a.d_final[(long long)w.b * a.D + c]
                     : 0.f;
             sE[col] = carry_in<C>(tl, w.tile, w.k, col, cuts ? kCut : accP, accC, first);
-        } else if (threadIdx.x < 2 * C) {  // the next: h, from every chunk's entry state
-            const int col = threadIdx.x - C;
+        } else if (tid < 2 * C) {  // the next: h, from every chunk's entry state
+            const int col = tid - C;
             bool owned;
             const int c = channel_of<V, NARROW>(w.cb, col, a.D, &owned);
             const int nC = (a.T + kGatedChunk - 1) / kGatedChunk;
@@ -799,8 +796,8 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
                     e = PACKED && (cuts >> r & 1) ? v : fmaf(p, e, v);
                 }
             }
-        } else if (threadIdx.x < 3 * C) {
-            if (part && before.k >= 0) sum_up(threadIdx.x - 2 * C);
+        } else if (tid < 3 * C) {
+            if (part && before.k >= 0) sum_up(tid - 2 * C);
         }
         __syncthreads();
         float h[V], G[V], db[V];
@@ -810,7 +807,7 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
             get<V>(&sC[w.r * C], w.cq, G);
             get<V>(&sR[w.r * C], w.cq, p);
             get<V>(sE, w.cq, in);
-            const bool cut = PACKED && w.r < RUNS - 1 && (cuts >> (w.r + 1));
+            const bool cut = PACKED && w.r < kRuns - 1 && (cuts >> (w.r + 1));
 #pragma unroll
             for (int i = 0; i < V; ++i) {
                 G[i] = cut ? G[i] : fmaf(p[i], in[i], G[i]);
@@ -865,7 +862,7 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
         if (part) {  // the wave's four runs; summed up during the next tile's scan
 #pragma unroll
             for (int i = 0; i < V; ++i) db[i] = row_sum(db[i]);
-            if (threadIdx.x % 64 < kLanes) put<V>(&sD[threadIdx.x / 64 * C], w.cq, db);
+            if (tid % 64 < kLanes) put<V>(&sD[tid / 64 * C], w.cq, db);
             before = w;
         }
         t = next;
@@ -882,6 +879,7 @@ __global__ __launch_bounds__(RUNS * kLanes, 4) void gated_bwd_kernel(GatedBwdArg
 // ---- small kernels ------------------------------------------------------------------------
 constexpr int kThreads = 256;
 constexpr int kStepVec = 4;
+constexpr int kPrepSeqs = 2048;
 
 // Before a pass: the counters cleared, spans and carries marked missing, the start bits of a packed row, and zero
 // final states for its empty sequences.
@@ -896,23 +894,34 @@ struct Prep {
     float* final_state;    // null: none
 };
 __global__ __launch_bounds__(kThreads) void gated_prep_kernel(Prep p) {
+    __shared__ int sCu[kPrepSeqs];
     const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
     const long long all = (long long)gridDim.x * kThreads;
     for (long long i = id; i < p.words / 4; i += all)
-        reinterpret_cast<uint4*>(p.clear)[i] = i < p.zeros / 4 ? make_uint4(0, 0, 0, 0)
-                                                       : make_uint4(~0u, ~0u, ~0u, ~0u);
+        __builtin_nontemporal_store(i < p.zeros / 4 ? Words<4>{0, 0, 0, 0}
+                                                    : Words<4>{~0u, ~0u, ~0u, ~0u},
+                                    reinterpret_cast<Words<4>*>(p.clear) + i);
     if (!p.starts) return;
-    for (long long i = id; i < p.bytes; i += all) {
-        int lo = 0, hi = p.nseq;  // first s with cu[s] >= 8 i
-        while (lo < hi) {
-            const int m = (lo + hi) / 2;
-            if (p.cu[m] >= 8 * i) hi = m; else lo = m + 1;
+    auto mark = [&](const int* cu) {
+        for (long long i = id; i < p.bytes; i += all) {
+            int lo = 0, hi = p.nseq;  // first s with cu[s] >= 8 i
+            while (lo < hi) {
+                const int m = (lo + hi) / 2;
+                if (cu[m] >= 8 * i) hi = m; else lo = m + 1;
+            }
+            unsigned bits = 0;
+            for (int s = lo; s < p.nseq && cu[s] < 8 * i + 8; ++s)
+                if (cu[s + 1] > cu[s]) bits |= 1u << (cu[s] - 8 * i);
+            p.starts[i] = (uint8_t)bits;
+            p.from[i] = lo;
         }
-        unsigned bits = 0;
-        for (int s = lo; s < p.nseq && p.cu[s] < 8 * i + 8; ++s)
-            if (p.cu[s + 1] > p.cu[s]) bits |= 1u << (p.cu[s] - 8 * i);
-        p.starts[i] = (uint8_t)bits;
-        p.from[i] = lo;
+    };
+    if (p.nseq < kPrepSeqs) {  // the search's steps wait for LDS then, not for memory
+        for (int i = threadIdx.x; i <= p.nseq; i += kThreads) sCu[i] = p.cu[i];
+        __syncthreads();
+        mark(sCu);
+    } else {
+        mark(p.cu);
     }
     if (!p.final_state) return;
     for (long long i = id; i < (long long)p.nseq * p.D; i += all) {
@@ -921,21 +930,22 @@ __global__ __launch_bounds__(kThreads) void gated_prep_kernel(Prep p) {
     }
 }
 
-// d_bias from the tiles' sums: a workgroup per 64 channels, 16 threads per channel; fixed
+// d_bias from the tiles' sums: a workgroup per 32 channels, 8 threads per channel; fixed
 // order.
-__global__ __launch_bounds__(1024) void gated_dbias_kernel(const float* part, float* d_bias,
-                                                           int rows, int D) {
-    __shared__ float s[16][64];
-    const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-    const int c = blockIdx.x * 64 + lane;
+__global__ __launch_bounds__(kThreads) void gated_dbias_kernel(const float* part, float* d_bias,
+                                                               int rows, int D) {
+    __shared__ float s[8][32];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const int c = blockIdx.x * 32 + lane;
     float v = 0.f;
     if (c < D)
 #pragma unroll 8
-        for (int r = w; r < rows; r += 16) v += part[(long long)r * D + c];
+        for (int r = w; r < rows; r += 8) v += part[(long long)r * D + c];
     s[w][lane] = v;
     __syncthreads();
     if (w != 0 || c >= D) return;
-    for (int i = 1; i < 16; ++i) v += s[i][lane];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) v += s[i][lane];
     d_bias[c] = v;
 }
 
@@ -1002,18 +1012,20 @@ Layout layout(int B, int T, int D, int steps, int cols) {
     l.bytes = l.part + (size_t)B * l.nk * D * sizeof(float);
     return l;
 }
-Layout fwd_layout(ssd_dtype dtype, int B, int T, int D) {
-    return layout(B, T, D, kFwdRuns * fwd_steps(dtype), kLanes * fwd_vec(dtype));
+Layout fwd_layout(ssd_dtype t, bool codes, int B, int T, int D) {
+    return layout(B, T, D, kRuns * fwd_steps(t, codes), kLanes * fwd_vec(t, codes));
 }
-Layout bwd_layout(ssd_dtype dtype, int B, int T, int D) {
-    return layout(B, T, D, kBwdRuns * bwd_steps(dtype), kLanes * bwd_vec(dtype));
+Layout bwd_layout(ssd_dtype t, int B, int T, int D) {
+    return layout(B, T, D, kRuns * bwd_steps(t), kLanes * kBwdVec);
 }
 Tiles tiles_of(const Layout& l, int B, int cols, char* ws, bool packed) {
     Tiles t = {};
     t.blocks = l.blocks;
     t.chains = B * l.blocks;
     t.nk = l.nk;
-    t.groups = t.chains >= 8 * (int)kCounters ? kCounters : 1;
+    // as many counters as share the chains out evenly, or nearly so
+    t.groups = kCounters;
+    while (t.chains % t.groups != 0 && t.chains < 8 * (int)t.groups) --t.groups;
     if (l.nk > 1) t.ticket = (unsigned*)ws;
     t.span = (unsigned long long*)(ws + kCounterBytes);
     t.block = t.span + l.tiles * cols;
@@ -1053,73 +1065,69 @@ size_t gated_workspace_bytes(int B, int T, int D) {
     if (B == 0 || T == 0 || D == 0) return 0;
     size_t most = 0;
     for (ssd_dtype t : {SSD_F32, SSD_BF16})
-        for (const Layout& l : {fwd_layout(t, B, T, D), bwd_layout(t, B, T, D)})
+        for (const Layout& l : {fwd_layout(t, false, B, T, D), fwd_layout(t, true, B, T, D),
+                                bwd_layout(t, B, T, D)})
             if (l.bytes > most) most = l.bytes;
     return most;
 }
 
 namespace {
 // As many workgroups as are resident at once, and no more per counter than its tiles.
-template <int RUNS, auto kern, typename... Args>
+template <auto kern, typename... Args>
 hipError_t launch_tiles(const Tiles& tl, hipStream_t st, Args... args) {
     static DeviceSlots slots;
     int grid = 0;
     const hipError_t e =
-        resident_grid((const void*)kern, RUNS * kLanes, 0, slots, &grid);
+        resident_grid((const void*)kern, kRuns * kLanes, 0, slots, &grid);
     if (e != hipSuccess) return e;
     const long long most =
         ((long long)tl.chains + tl.groups - 1) / tl.groups * tl.nk * tl.groups;
     if (grid > most) grid = (int)most;
-    kern<<<grid, RUNS * kLanes, 0, st>>>(args...);
+    kern<<<grid, kRuns * kLanes, 0, st>>>(args...);
     return hipGetLastError();
 }
 
-template <typename T, ssd_dtype DT, bool NARROW>
+template <typename T, ssd_dtype DT, bool CODES, bool NARROW>
 hipError_t run_fwd(const GatedFwdArgs& a, char* ws, hipStream_t st) {
-    constexpr int V = fwd_vec(DT), S = fwd_steps(DT);
-    const Layout l = fwd_layout(DT, a.B, a.T, a.D);
-    hipError_t e = prepare(l, ws, a.cu, a.nseq, a.T, a.D, a.final_state, st);
+    constexpr int V = fwd_vec(DT, CODES), S = fwd_steps(DT, CODES);
+    const Layout l = fwd_layout(DT, CODES, a.B, a.T, a.D);
+    const hipError_t e = prepare(l, ws, a.cu, a.nseq, a.T, a.D, a.final_state, st);
     if (e != hipSuccess) return e;
     const Tiles tl = tiles_of(l, a.B, kLanes * V, ws, a.cu != nullptr);
-    const bool codes = a.x_codes != nullptr;
-#define SSD_GATED_FWD(PACKED, CODES) \
-    launch_tiles<kFwdRuns, gated_fwd_kernel<T, V, S, kFwdRuns, PACKED, CODES, NARROW>>(tl, st, a, tl)
-    if (a.cu) return codes ? SSD_GATED_FWD(true, true) : SSD_GATED_FWD(true, false);
-    return codes ? SSD_GATED_FWD(false, true) : SSD_GATED_FWD(false, false);
-#undef SSD_GATED_FWD
+    return a.cu ? launch_tiles<gated_fwd_kernel<T, V, S, true, CODES, NARROW>>(tl, st, a, tl)
+                : launch_tiles<gated_fwd_kernel<T, V, S, false, CODES, NARROW>>(tl, st, a, tl);
 }
 
-template <typename T, ssd_dtype DT, bool NARROW>
+template <typename T, ssd_dtype DT, bool CODES, bool NARROW>
 hipError_t run_bwd(const GatedBwdArgs& a, char* ws, hipStream_t st) {
-    constexpr int V = bwd_vec(DT), S = bwd_steps(DT);
+    constexpr int V = kBwdVec, S = bwd_steps(DT);
     const Layout l = bwd_layout(DT, a.B, a.T, a.D);
     hipError_t e = prepare(l, ws, a.cu, a.nseq, a.T, a.D, nullptr, st);
     if (e != hipSuccess) return e;
     const Tiles tl = tiles_of(l, a.B, kLanes * V, ws, a.cu != nullptr);
     const int rows = a.B * l.nk;
     float* part = !a.d_bias ? nullptr : rows == 1 ? a.d_bias : (float*)(ws + l.part);
-    const bool codes = a.x_codes != nullptr;
-#define SSD_GATED_BWD(PACKED, CODES) \
-    launch_tiles<kBwdRuns, gated_bwd_kernel<T, V, S, kBwdRuns, PACKED, CODES, NARROW>>(tl, st, a, tl, part)
-    if (a.cu) e = codes ? SSD_GATED_BWD(true, true) : SSD_GATED_BWD(true, false);
-    else e = codes ? SSD_GATED_BWD(false, true) : SSD_GATED_BWD(false, false);
-#undef SSD_GATED_BWD
+    e = a.cu ? launch_tiles<gated_bwd_kernel<T, V, S, true, CODES, NARROW>>(tl, st, a, tl, part)
+             : launch_tiles<gated_bwd_kernel<T, V, S, false, CODES, NARROW>>(tl, st, a, tl, part);
     if (e != hipSuccess || !a.d_bias || rows == 1) return e;
-    gated_dbias_kernel<<<(unsigned)((a.D + 63) / 64), 1024, 0, st>>>(part, a.d_bias, rows, a.D);
+    gated_dbias_kernel<<<(unsigned)((a.D + 31) / 32), kThreads, 0, st>>>(part, a.d_bias, rows,
+                                                                         a.D);
     return hipGetLastError();
 }
 
-// fn<T, dtype, NARROW>(a, ws, st): rows narrower than a piece have forms of their own
-#define SSD_GATED_RUN(fn, vec)                                                         \
-    (dtype == SSD_F32 ? (a.D < vec(SSD_F32) ? fn<float, SSD_F32, true>(a, (char*)ws, st)      \
-                                            : fn<float, SSD_F32, false>(a, (char*)ws, st))    \
-                      : (a.D < vec(SSD_BF16) ? fn<__bf16, SSD_BF16, true>(a, (char*)ws, st)   \
-                                             : fn<__bf16, SSD_BF16, false>(a, (char*)ws, st)))
+// run<T, dtype, CODES, NARROW>(a, ws, st): rows narrower than a piece have forms of their own
+#define SSD_GATED_RUN(run, T, DT, vec)                                                       \
+    (a.x_codes ? (a.D < vec(DT, true) ? run<T, DT, true, true>(a, (char*)ws, st)             \
+                                      : run<T, DT, true, false>(a, (char*)ws, st))           \
+               : (a.D < vec(DT, false) ? run<T, DT, false, true>(a, (char*)ws, st)           \
+                                       : run<T, DT, false, false>(a, (char*)ws, st)))
+constexpr int bwd_vec(ssd_dtype, bool) { return kBwdVec; }
 }  // namespace
 
 hipError_t launch_gated_fwd(ssd_dtype dtype, const GatedFwdArgs& a, void* ws, hipStream_t st) {
     if (a.T > 0)
-        return SSD_GATED_RUN(run_fwd, fwd_vec);
+        return dtype == SSD_F32 ? SSD_GATED_RUN(run_fwd, float, SSD_F32, fwd_vec)
+                                : SSD_GATED_RUN(run_fwd, __bf16, SSD_BF16, fwd_vec);
     if (!a.final_state) return hipSuccess;
     const long long n = (long long)(a.cu ? a.nseq : a.B) * a.D;
     gated_carry_kernel<<<blocks_of(n), kThreads, 0, st>>>(a.init, a.final_state, n);
@@ -1128,7 +1136,8 @@ hipError_t launch_gated_fwd(ssd_dtype dtype, const GatedFwdArgs& a, void* ws, hi
 
 hipError_t launch_gated_bwd(ssd_dtype dtype, const GatedBwdArgs& a, void* ws, hipStream_t st) {
     if (a.T > 0 && a.B > 0)
-        return SSD_GATED_RUN(run_bwd, bwd_vec);
+        return dtype == SSD_F32 ? SSD_GATED_RUN(run_bwd, float, SSD_F32, bwd_vec)
+                                : SSD_GATED_RUN(run_bwd, __bf16, SSD_BF16, bwd_vec);
     const long long n = (long long)a.B * a.D;
     if (a.d_init && n > 0)
         gated_carry_kernel<<<blocks_of(n), kThreads, 0, st>>>(a.d_final, a.d_init, n);
