@@ -6,6 +6,7 @@ HIP stream go to the C ABI.  Every step of the computation runs in libssd's kern
 there is no fallback of any kind: if libssd.so is missing the first call raises.
 """
 import ctypes
+import functools
 import os
 
 import torch
@@ -830,10 +831,9 @@ def _addr(t):
 
 def _flat(t, name, dtype, dev, shape):
     """The address of a contiguous tensor with exactly this dtype, device and shape."""
-    if t is not None and t.dtype is dtype and t.device == dev and t.shape == shape \
-            and t.is_contiguous():
-        return t.data_ptr()
-    _shape(_need(t, name, dtype, dev), name, shape)
+    if t is None or t.dtype is not dtype or t.device != dev or t.shape != shape \
+            or not t.is_contiguous():
+        _shape(_need(t, name, dtype, dev), name, shape)  # says which
     return t.data_ptr()
 
 
@@ -847,11 +847,16 @@ def _rows(t, name, dtype=None, device=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if device is not None and t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    shape = t.shape
+    shape, strides = t.shape, t.stride()
     width = shape[-1]
+    if strides[-1] == 1:  # the usual cases: [rows, width] and [batch, steps, width]
+        if len(shape) == 2 and shape[0] > 1 and strides[0] >= width:
+            return strides[0]
+        if len(shape) == 3 and shape[1] > 1 and strides[1] >= width and \
+                (shape[0] == 1 or strides[0] == shape[1] * strides[1]):
+            return strides[1]
     if t.is_contiguous() or t.numel() == 0:
         return width
-    strides = t.stride()
     if width > 1 and strides[-1] != 1:
         raise ValueError(f"{name} must have contiguous rows")
     stride, span = width, None  # span: what the next leading dimension's stride has to be
@@ -992,10 +997,23 @@ def ssd_gated_workspace_size(dims):
     return int(library().ssd_gated_workspace_size(ctypes.byref(dims)))
 
 
+@functools.lru_cache(maxsize=256)
+def _gated_ref(batch, seqlen, channels):
+    """A reference to the dims of these sizes (the library only reads them)."""
+    return ctypes.byref(SsdGatedDims(batch, seqlen, channels))
+
+
 def _gated_dims(x, name="x"):
     if x.dim() != 3:
         raise ValueError(f"{name} must be [B, T, channels], got {tuple(x.shape)}")
     return SsdGatedDims(*x.shape)
+
+
+def _gated_shape(x, name="x"):
+    shape = x.shape
+    if len(shape) != 3:
+        raise ValueError(f"{name} must be [B, T, channels], got {tuple(shape)}")
+    return shape
 
 
 def ssd_gated_workspace(x):
@@ -1034,31 +1052,34 @@ def _gated_saved(saved, dev, shape, codes):
                                   for n, (dty, kshape) in zip(names, kinds)))
 
 
-def _gated_common(dims, dev, bias, cu_seqlens, check):
+def _gated_common(shape, dev, bias, cu_seqlens, check):
     """(address of bias, number of sequences, rows of a final state), bias and cu_seqlens
     checked."""
     if bias is not None:
-        bias = _flat(bias, "bias", torch.float32, dev, (dims.channels,))
+        bias = _flat(bias, "bias", torch.float32, dev, shape[2:])
     if cu_seqlens is None:
-        return bias, 0, dims.batch
+        return bias, 0, shape[0]
     _need(cu_seqlens, "cu_seqlens", torch.int32, dev)
     if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
         raise ValueError("cu_seqlens must be [nseq + 1] with nseq >= 1")
-    if dims.batch != 1:
+    if shape[0] != 1:
         raise ValueError("a packed row has batch 1")
     if check:
         cu = cu_seqlens.cpu()
-        if int(cu[0]) != 0 or int(cu[-1]) != dims.seqlen or bool((cu[1:] < cu[:-1]).any()):
-            raise ValueError(f"cu_seqlens must rise from 0 to T = {dims.seqlen}")
+        if int(cu[0]) != 0 or int(cu[-1]) != shape[1] or bool((cu[1:] < cu[:-1]).any()):
+            raise ValueError(f"cu_seqlens must rise from 0 to T = {shape[1]}")
     nseq = cu_seqlens.numel() - 1
     return bias, nseq, nseq
 
 
-def _gated_workspace(workspace, dims, dev):
+def _gated_workspace(workspace, shape, dev):
+    """(address, bytes); without a workspace one is allocated, and kept by the third."""
     if workspace is None:
-        workspace = torch.empty(max(ssd_gated_workspace_size(dims), 1), dtype=torch.uint8,
-                                device=dev)
-    return _need(workspace, "workspace", device=dev)
+        workspace = torch.empty(max(ssd_gated_workspace_size(SsdGatedDims(*shape)), 1),
+                                dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        _need(workspace, "workspace", device=dev)
+    return workspace.data_ptr(), workspace.nbytes, workspace
 
 
 def ssd_gated_fwd(x, g, bias=None, init_state=None, cu_seqlens=None, saved=None, h=None,
@@ -1071,14 +1092,14 @@ def ssd_gated_fwd(x, g, bias=None, init_state=None, cu_seqlens=None, saved=None,
     buffers of ssd_gated_saved(x), filled for the backward.  cu_seqlens int32 [nseq + 1] on
     the device: a packed row (B = 1), final_state [nseq, channels]; it is copied to the host
     and checked unless check_cu_seqlens is False (which waits for the stream)."""
-    dims, dev, f32, shape = _gated_dims(x), x.device, torch.float32, x.shape
+    shape, dev, f32 = _gated_shape(x), x.device, torch.float32
     if stream is not None:
         return _on(stream, dev, ssd_gated_fwd, x, g, bias, init_state, cu_seqlens, saved, h,
                    final_state, want_final, workspace, check_cu_seqlens)
     code, dtype = _code_of(x, "x"), x.dtype
     xs, gs = _rows(x, "x"), _rows(g, "g", dtype, dev)
     _shape(g, "g", shape)
-    pb, nseq, ends = _gated_common(dims, dev, bias, cu_seqlens, check_cu_seqlens)
+    pb, nseq, ends = _gated_common(shape, dev, bias, cu_seqlens, check_cu_seqlens)
     pi = pf = sv = None
     if init_state is not None:
         pi = _flat(init_state, "init_state", f32, dev, (shape[0], shape[2]))
@@ -1089,22 +1110,22 @@ def ssd_gated_fwd(x, g, bias=None, init_state=None, cu_seqlens=None, saved=None,
         pf = _flat(final_state, "final_state", f32, dev, (ends, shape[2]))
     if saved is not None:
         sv = ctypes.byref(_gated_saved(saved, dev, shape, None))
-    workspace = _gated_workspace(workspace, dims, dev)
-    _launch(library().ssd_gated_fwd, dev, ctypes.byref(dims), code, x.data_ptr(), xs,
+    pw, nbytes, workspace = _gated_workspace(workspace, shape, dev)
+    _launch(library().ssd_gated_fwd, dev, _gated_ref(*shape), code, x.data_ptr(), xs,
             g.data_ptr(), gs, pb, _addr(cu_seqlens), nseq, pi, _flat(h, "h", dtype, dev, shape),
-            pf, sv, workspace.data_ptr(), _nbytes(workspace))
+            pf, sv, pw, nbytes)
     return h, final_state
 
 
-def _gated_bwd(fn, inputs, dims, shape, dtype, dev, bias, dh, saved, d_final, cu_seqlens,
+def _gated_bwd(fn, inputs, shape, dtype, dev, bias, dh, saved, d_final, cu_seqlens,
                want_d_bias, want_d_init, out, workspace, check):
     f32 = torch.float32
     hs = _rows(dh, "dh", dtype, dev)
     _shape(dh, "dh", shape)
-    pb, nseq, ends = _gated_common(dims, dev, bias, cu_seqlens, check)
+    pb, nseq, ends = _gated_common(shape, dev, bias, cu_seqlens, check)
     pf = None
     if d_final is not None:
-        pf = _flat(d_final, "d_final", f32, dev, (ends, dims.channels))
+        pf = _flat(d_final, "d_final", f32, dev, (ends, shape[2]))
     sv = _gated_saved(saved, dev, shape, not inputs)
     o = dict(out or {})
     for k in ("dx", "dg"):
@@ -1114,17 +1135,17 @@ def _gated_bwd(fn, inputs, dims, shape, dtype, dev, bias, dh, saved, d_final, cu
     strides = [_rows(o[k], k, dtype, dev) for k in ("dx", "dg")]
     want_d_init = want_d_init and cu_seqlens is None
     sums = []
-    for k, want, kshape in (("d_bias", want_d_bias, (dims.channels,)),
-                            ("d_init", want_d_init, (dims.batch, dims.channels))):
+    for k, want, kshape in (("d_bias", want_d_bias, shape[2:]),
+                            ("d_init", want_d_init, (shape[0], shape[2]))):
         if not want:
             o[k] = None
         elif o.get(k) is None:
             o[k] = torch.empty(kshape, dtype=f32, device=dev)
         sums.append(_flat(o[k], k, f32, dev, kshape) if want else None)
-    workspace = _gated_workspace(workspace, dims, dev)
-    _launch(fn, dev, ctypes.byref(dims), _DTYPE_CODE[dtype], *inputs, pb, _addr(cu_seqlens), nseq,
+    pw, nbytes, workspace = _gated_workspace(workspace, shape, dev)
+    _launch(fn, dev, _gated_ref(*shape), _DTYPE_CODE[dtype], *inputs, pb, _addr(cu_seqlens), nseq,
             ctypes.byref(sv), dh.data_ptr(), hs, pf, o["dx"].data_ptr(), strides[0],
-            o["dg"].data_ptr(), strides[1], *sums, workspace.data_ptr(), _nbytes(workspace))
+            o["dg"].data_ptr(), strides[1], *sums, pw, nbytes)
     return o
 
 
@@ -1136,15 +1157,15 @@ def ssd_gated_bwd(x, g, bias, dh, saved, d_final=None, cu_seqlens=None, want_d_b
     dict with dx, dg, d_bias and d_init (None where not wanted, and d_init for a packed
     row).  out may hold preallocated tensors under those names; dx and dg may be column
     ranges of one gradient of the projection's output."""
-    dims, dev = _gated_dims(x), x.device
+    shape, dev = _gated_shape(x), x.device
     if stream is not None:
         return _on(stream, dev, ssd_gated_bwd, x, g, bias, dh, saved, d_final, cu_seqlens,
                    want_d_bias, want_d_init, out, workspace, check_cu_seqlens)
     _code_of(x, "x")
     xs, gs = _rows(x, "x"), _rows(g, "g", x.dtype, dev)
-    _shape(g, "g", x.shape)
-    return _gated_bwd(library().ssd_gated_bwd, (x.data_ptr(), xs, g.data_ptr(), gs), dims,
-                      x.shape, x.dtype, dev, bias, dh, saved, d_final, cu_seqlens, want_d_bias,
+    _shape(g, "g", shape)
+    return _gated_bwd(library().ssd_gated_bwd, (x.data_ptr(), xs, g.data_ptr(), gs), shape,
+                      x.dtype, dev, bias, dh, saved, d_final, cu_seqlens, want_d_bias,
                       want_d_init, out, workspace, check_cu_seqlens)
 
 
@@ -1153,13 +1174,13 @@ def ssd_gated_bwd_ckpt(bias, dh, saved, d_final=None, cu_seqlens=None, want_d_bi
                        stream=None):
     """ssd_gated_bwd from the 8-bit checkpoints of x and g in saved (libssd.ssd_gated_bwd_ckpt:
     ssd_gated_saved(x, ckpt=True), filled by ssd_gated_fwd)."""
-    dims = _gated_dims(dh, "dh")
+    shape = _gated_shape(dh, "dh")
     if stream is not None:
         return _on(stream, dh.device, ssd_gated_bwd_ckpt, bias, dh, saved, d_final, cu_seqlens,
                    want_d_bias, want_d_init, out, workspace, check_cu_seqlens)
     _code_of(dh, "dh")
-    return _gated_bwd(library().ssd_gated_bwd_ckpt, (), dims, dh.shape, dh.dtype, dh.device, bias,
-                      dh, saved, d_final, cu_seqlens, want_d_bias, want_d_init, out, workspace,
+    return _gated_bwd(library().ssd_gated_bwd_ckpt, (), shape, dh.dtype, dh.device, bias, dh,
+                      saved, d_final, cu_seqlens, want_d_bias, want_d_init, out, workspace,
                       check_cu_seqlens)
 
 
@@ -1167,15 +1188,15 @@ def ssd_gated_step(x, g, bias, state, h=None, stream=None):
     """One step of the gated recurrence (libssd.ssd_gated_step): x, g [batch, channels] (rows
     may be column ranges), state [batch, channels] fp32 (updated in place).  Returns h in
     x's dtype."""
-    if x.dim() != 2:
-        raise ValueError(f"x must be [batch, channels], got {tuple(x.shape)}")
     dev, shape, dtype, f32 = x.device, x.shape, x.dtype, torch.float32
+    if len(shape) != 2:
+        raise ValueError(f"x must be [batch, channels], got {tuple(shape)}")
     if stream is not None:
         return _on(stream, dev, ssd_gated_step, x, g, bias, state, h)
     code, xs, gs = _code_of(x, "x"), _rows(x, "x"), _rows(g, "g", dtype, dev)
     _shape(g, "g", shape)
     h = torch.empty(shape, dtype=dtype, device=dev) if h is None else h
-    _launch(library().ssd_gated_step, dev, ctypes.byref(SsdGatedDims(shape[0], 1, shape[1])), code,
+    _launch(library().ssd_gated_step, dev, _gated_ref(shape[0], 1, shape[1]), code,
             x.data_ptr(), xs, g.data_ptr(), gs,
             None if bias is None else _flat(bias, "bias", f32, dev, (shape[1],)),
             _flat(state, "state", f32, dev, shape), _flat(h, "h", dtype, dev, shape))
