@@ -45,7 +45,9 @@ struct CkptScale {
         const bool tiny = most < 0x0d800000u;        // below 2^-100: 127 / m could overflow
         const bool finite = most < 0x7f800000u;
         // at most the largest fp32 value that 127 times stays finite
-        scale = tiny ? 0.f : finite ? fminf(m / 127.f, 0x1.0204060000000p+121f) : __uint_as_float(0x7fc00000u);
+        scale = tiny     ? 0.f
+                : finite ? fminf(m / 127.f, 0x1.020406p+121f)
+                         : __uint_as_float(0x7fc00000u);
         inverse = tiny || !finite ? 0.f : 127.f / m;
     }
 };

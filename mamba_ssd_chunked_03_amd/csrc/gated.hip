@@ -6,24 +6,29 @@
 //
 // Both recursions are affine in what they carry: over a span of steps the carry v becomes
 // H + P v, with P the product of the span's a and H its result from zero, and two spans
-// combine to (P2 P1, H2 + P2 H1).  A workgroup owns a tile of 256 bytes of channels and 32
-// runs of S steps; one pass over HBM:
-//   1. every thread loads its run (S steps of the neighbouring channels that 16 bytes hold)
-//      into registers and forms the run's (P, H);
-//   2. a lane per channel scans the 32 runs through LDS into prefixes and the
-//      tile's own (P, H), and finds the carry into the tile: the tiles of one chain (batch
-//      element and channels) publish their (P, H), every 16th also the carry out of it,
-//      and a tile combines the last such carry with the spans behind it;
+// combine to (P2 P1, H2 + P2 H1).  A workgroup works on a tile of 16 lanes' pieces of a row
+// (64 or 128 channels) by 32 runs of S steps, in one pass over HBM:
+//   1. every thread loads its run (S steps of its piece) into registers and forms the run's
+//      (P, H);
+//   2. a lane per channel scans the 32 runs through LDS into prefixes and the tile's own
+//      (P, H), publishes that, and finds the carry into the tile from what the tiles before
+//      it in its chain (batch element and channels) have published;
 //   3. every thread takes its run's carry and goes through the run again, from registers.
 // The backward does this for h from the saved entry states (no waiting) and, last step
-// first, for G.  Bound by HBM: 3 (forward) or 5 (backward) values per element in and out.
+// first, for G.
+//
+// Bound by HBM: 3 (forward) or 5 (backward) values per element in and out.  At 4 x 4096 x 5120
+// in bf16 the forward takes 100 us (503 MB, 5.0 TB/s: what a large copy reaches here) and the
+// backward 182 us (839 MB, 4.6 TB/s); a forward in three kernels would read x and g twice, 5
+// values per element.  One tile alone takes 5.5 us from launch to end; what lies between
+// that and HBM's time at medium sizes is the wait for the carry and the prep launch (2 us).
 //
 // Waiting ends: tiles are numbered so that a chain's tiles follow in carry order, and a
-// workgroup takes its number from a counter when it starts, so every tile that it waits for
-// was taken by a workgroup that already runs; that one publishes its (P, H) before it
-// waits itself, and the carry out of a 16th tile waits for earlier tiles only.  A published
-// word holds the value and a tag in one 64-bit atomic store, so a reader that sees the tag
-// has the value, whatever the order of other stores.
+// workgroup takes numbers from a counter, the next one while it works on a tile.  Of all
+// tiles not finished the one with the lowest number in its counter is being worked on (a
+// workgroup works on its numbers in order), and what it waits for was published by finished
+// tiles, or by later parts of none: a tile publishes its own (P, H) before it waits.  So it
+// ends, whatever share of the workgroups is on the device.
 #include <initializer_list>
 
 #include "gated.h"
@@ -190,10 +195,13 @@ struct Tiles {
     const int* from;                   // and per byte of these: the first s with cu[s] >= 8 i
     int chains, blocks, nk;            // B * blocks, channel blocks, tiles of a chain
     unsigned groups;                   // counters in use
+    unsigned* done;                    // d_bias: tiles of a channel block that are through
 };
 
 // A word not yet published has all bits set: a NaN that no published value can be, since a
-// NaN is published as the one below.  A span is one 64-bit store, so it is seen whole.
+// NaN is published as the one below.  A span is one 64-bit store, so it is seen whole, and
+// nothing rests on the order of two stores.  All of these words are read and written at the
+// device's scope, past the XCDs' own L2 caches.
 constexpr unsigned kNotYet = 0xffffffffu;
 __device__ __forceinline__ unsigned bits_of(float v) {
     return v == v ? __float_as_uint(v) : 0x7fc00000u;
@@ -427,9 +435,9 @@ template <typename T, int V, int S, bool PACKED, bool CODES, bool NARROW>
 __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_fwd_kernel(GatedFwdArgs a, Tiles tl) {
     constexpr int C = kLanes * V, kTile = kRuns * S;
     __shared__ __align__(16) float sP[kRuns * C], sH[kRuns * C], sE[C];
-    __shared__ unsigned sNext, sCut[kRuns];
+    __shared__ unsigned sFirst, sNext, sCut[kRuns];
     const Group group = group_of(tl);
-    unsigned t = first_number(tl, group, &sNext);
+    unsigned t = first_number(tl, group, &sFirst);
     if (t >= group.tiles) return;
     Place w;
     Piece<T, V> x[S], g[S];
@@ -564,11 +572,10 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_fwd_kernel(GatedFwdAr
                     store<T, V>((T*)((char*)((T*)a.h + (row0 + j) * a.D) +
                                      row_offset<T>(w.r * S, a.D, w.o.c0)),
                                 h, w.o);
-                if (PACKED && a.final_state && (ends >> j & 1))
-                    store<float, V>(a.final_state +
-                                        (long long)sequence_ending(a.cu, a.nseq, from, ts + j) * a.D +
-                                        w.o.c0,
-                                    h, w.o);
+                if (PACKED && a.final_state && (ends >> j & 1)) {
+                    const long long seq = sequence_ending(a.cu, a.nseq, from, ts + j);
+                    store<float, V>(a.final_state + seq * a.D + w.o.c0, h, w.o);
+                }
             }
             if (!PACKED && a.final_state && ts <= a.T - 1 && a.T - 1 < ts + S)
                 store<float, V>(a.final_state + (long long)w.b * a.D + w.o.c0, h, w.o);
@@ -641,11 +648,12 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
     constexpr int kChunkRuns = kGatedChunk / S;
     static_assert(kTile % kGatedChunk == 0 && kRuns * kLanes >= 3 * C, "tiles hold whole chunks");
     constexpr int kWaves = kRuns * kLanes / 64;
-    __shared__ __align__(16) float sP[kRuns * C], sH[kRuns * C], sC[kRuns * C], sR[kRuns * C], sE[C];
+    __shared__ __align__(16) float sP[kRuns * C], sH[kRuns * C], sC[kRuns * C], sR[kRuns * C];
+    __shared__ __align__(16) float sE[C];
     __shared__ __align__(16) float sD[kWaves * C];  // d_bias' share of every wave
-    __shared__ unsigned sNext, sCut[kRuns];
+    __shared__ unsigned sFirst, sNext, sCut[kRuns];
     const Group group = group_of(tl);
-    unsigned t = first_number(tl, group, &sNext);
+    unsigned t = first_number(tl, group, &sFirst);
     if (t >= group.tiles) return;
     Place w;
     RunIn<T, V, S, CODES, NARROW> x, g;
@@ -665,13 +673,46 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
     };
     Place before;  // the tile whose shares of d_bias are in sD
     before.k = -1;
+    // one wave; with tl.done the last tile of the channel block adds up all of them
     auto sum_up = [&](int col) {
         bool owned;
         const int c = channel_of<V, NARROW>(before.cb, col, a.D, &owned);
         float s = 0.f;
 #pragma unroll
         for (int i = 0; i < kWaves; ++i) s += sD[i * C + col];
-        if (owned) part[((long long)before.b * tl.nk + tl.nk - 1 - before.k) * a.D + c] = s;
+        const int tiles = a.B * tl.nk;
+        unsigned* to = (unsigned*)part + ((long long)before.b * tl.nk + tl.nk - 1 - before.k) * a.D;
+        if (!tl.done) {
+            if (owned) to[c] = __float_as_uint(s);
+            return;
+        }
+        if (owned)
+            __hip_atomic_store(to + c, bits_of(s), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        unsigned through = 0;
+        if (col == 0) through = atomicAdd(tl.done + before.cb, 1u);
+        if ((int)__builtin_amdgcn_readfirstlane(through) != tiles - 1) return;
+        // the others' sums are there, or stored and on their way
+        const unsigned* from = (const unsigned*)part + c;
+        s = 0.f;
+        for (int r0 = 0; r0 < tiles; r0 += 8) {
+            unsigned v[8];
+            for (;;) {
+                bool all = true;
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    v[r] = owned && r0 + r < tiles
+                               ? __hip_atomic_load(from + (long long)(r0 + r) * a.D,
+                                                   __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                               : 0u;
+#pragma unroll
+                for (int r = 0; r < 8; ++r) all = all && v[r] != kNotYet;
+                if (__all(all)) break;
+                __builtin_amdgcn_s_sleep(1);
+            }
+#pragma unroll
+            for (int r = 0; r < 8; ++r) s += __uint_as_float(v[r]);
+        }
+        if (owned) a.d_bias[c] = s;
     };
     fetch();
     for (;;) {
@@ -701,12 +742,12 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
         }
         // d_final of a packed sequence that ends at step j of this run
         auto ending = [&](int j, float (&v)[V]) {
-            load_f32<V, NARROW>(
-                v,
-                a.d_final
-                    ? a.d_final + (long long)sequence_ending(a.cu, a.nseq, from, ts + j) * a.D + w.o.c0
-                    : nullptr,
-                w.o);
+            const float* d = nullptr;
+            if (a.d_final) {
+                const long long seq = sequence_ending(a.cu, a.nseq, from, ts + j);
+                d = a.d_final + seq * a.D + w.o.c0;
+            }
+            load_f32<V, NARROW>(v, d, w.o);
         };
         {
             // G's carry out of the run in the same sweep: dh_j reaches it through the product
@@ -881,8 +922,8 @@ constexpr int kThreads = 256;
 constexpr int kStepVec = 4;
 constexpr int kPrepSeqs = 2048;
 
-// Before a pass: the counters cleared, spans and carries marked missing, the start bits of a packed row, and zero
-// final states for its empty sequences.
+// Before a pass: the counters cleared, spans and carries marked missing, the start bits of a
+// packed row, and zero final states for its empty sequences.
 struct Prep {
     unsigned* clear;       // counters, then spans and carries: words to set
     long long zeros, words;  // the first to 0, the others to kNotYet
@@ -930,7 +971,7 @@ __global__ __launch_bounds__(kThreads) void gated_prep_kernel(Prep p) {
     }
 }
 
-// d_bias from the tiles' sums: a workgroup per 32 channels, 8 threads per channel; fixed
+// d_bias from the tiles' sums, where there are many: a workgroup per 32 channels, 8 threads per channel; fixed
 // order.
 __global__ __launch_bounds__(kThreads) void gated_dbias_kernel(const float* part, float* d_bias,
                                                                int rows, int D) {
@@ -988,35 +1029,46 @@ __global__ __launch_bounds__(kThreads) void gated_step_kernel(GatedStepArgs a, u
 
 unsigned blocks_of(long long n) { return (unsigned)((n + kThreads - 1) / kThreads); }
 
-// ---- workspace: counters and spans | start bits, sequences | d_bias' sums -------------------------------
+// ---- workspace: counters | spans (and d_bias' sums) | start bits, sequences | (d_bias' sums) --
 struct Layout {
     int nk, blocks;
+    bool fused;                        // the last tile of a channel block makes d_bias
     long long tiles, spans, carries;  // tiles; spans of one and of 16; carries
-    size_t clear, starts, part, bytes;  // sizes of the first two; offset of the third; total
+    // sizes of what prep clears to zero, of all that it sets, of the start bits; offset of
+    // d_bias' sums; total
+    size_t zeros, clear, starts, part, bytes;
 };
 constexpr size_t kCounterBytes = kCounters * kCounterWords * 4;
+// d_bias from its tiles' sums: with so many tiles to a channel block or fewer the last one adds
+// them up (2 x 1003 x 1001 in fp32, 16 tiles: 17.7 us, 20.0 with a kernel of its own), behind
+// that a kernel of its own does (4 x 4096 x 5120, 64 tiles: 189 and 183; 32 tiles: equal).
+constexpr long long kFusedTiles = 16;
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // tiles of `steps` steps and `cols` channels
-Layout layout(int B, int T, int D, int steps, int cols) {
+Layout layout(int B, int T, int D, int steps, int cols, bool bwd) {
     Layout l;
     l.nk = (T + steps - 1) / steps;
     l.blocks = (D + cols - 1) / cols;
     l.tiles = (long long)B * l.blocks * l.nk;
-    const long long chains = (long long)B * l.blocks;
+    const long long chains = (long long)B * l.blocks, rows = (long long)B * l.nk;
     l.spans = l.tiles + chains * (l.nk / kBlockTiles);
-    l.carries = (chains * (l.nk / (kBlockTiles * kBlockTiles)) + 1) / 2 * 2;
-    l.clear = kCounterBytes +
-              (l.nk > 1 ? (size_t)(l.spans * 2 + l.carries) * cols * sizeof(unsigned) : 0);
+    l.carries = (chains * (l.nk / (kBlockTiles * kBlockTiles)) + 3) / 4 * 4;
+    l.fused = bwd && l.nk > 1 && rows <= kFusedTiles;
+    l.zeros = kCounterBytes + (l.fused ? up256((size_t)l.blocks * sizeof(unsigned)) : 0);
+    const size_t sums = up256((size_t)rows * D * sizeof(float));
+    l.clear = l.zeros + (l.nk > 1 ? up256((size_t)(l.spans * 2 + l.carries) * cols * 4) : 0);
+    l.part = l.clear;
+    if (l.fused) l.clear += sums;
     l.starts = up256((size_t)l.nk * ((steps + 7) / 8) + 1);
-    l.part = l.clear + l.starts * 5;
-    l.bytes = l.part + (size_t)B * l.nk * D * sizeof(float);
+    if (!l.fused) l.part = l.clear + l.starts * 5;
+    l.bytes = l.clear + l.starts * 5 + (bwd && !l.fused ? sums : 0);
     return l;
 }
 Layout fwd_layout(ssd_dtype t, bool codes, int B, int T, int D) {
-    return layout(B, T, D, kRuns * fwd_steps(t, codes), kLanes * fwd_vec(t, codes));
+    return layout(B, T, D, kRuns * fwd_steps(t, codes), kLanes * fwd_vec(t, codes), false);
 }
 Layout bwd_layout(ssd_dtype t, int B, int T, int D) {
-    return layout(B, T, D, kRuns * bwd_steps(t), kLanes * kBwdVec);
+    return layout(B, T, D, kRuns * bwd_steps(t), kLanes * kBwdVec, true);
 }
 Tiles tiles_of(const Layout& l, int B, int cols, char* ws, bool packed) {
     Tiles t = {};
@@ -1027,7 +1079,8 @@ Tiles tiles_of(const Layout& l, int B, int cols, char* ws, bool packed) {
     t.groups = kCounters;
     while (t.chains % t.groups != 0 && t.chains < 8 * (int)t.groups) --t.groups;
     if (l.nk > 1) t.ticket = (unsigned*)ws;
-    t.span = (unsigned long long*)(ws + kCounterBytes);
+    if (l.fused) t.done = (unsigned*)(ws + kCounterBytes);
+    t.span = (unsigned long long*)(ws + l.zeros);
     t.block = t.span + l.tiles * cols;
     t.carry = (unsigned*)(t.span + l.spans * cols);
     if (packed) {
@@ -1041,7 +1094,7 @@ hipError_t prepare(const Layout& l, char* ws, const int* cu, int nseq, int T, in
     if (l.nk <= 1 && !cu) return hipSuccess;
     Prep p = {};
     p.clear = (unsigned*)ws;
-    p.zeros = kCounters * kCounterWords;
+    p.zeros = (long long)(l.zeros / 4);
     p.words = (long long)(l.clear / 4);
     long long work = p.words / 4;
     if (cu) {
@@ -1083,6 +1136,7 @@ hipError_t launch_tiles(const Tiles& tl, hipStream_t st, Args... args) {
     const long long most =
         ((long long)tl.chains + tl.groups - 1) / tl.groups * tl.nk * tl.groups;
     if (grid > most) grid = (int)most;
+    grid -= grid % tl.groups;
     kern<<<grid, kRuns * kLanes, 0, st>>>(args...);
     return hipGetLastError();
 }
@@ -1109,7 +1163,7 @@ hipError_t run_bwd(const GatedBwdArgs& a, char* ws, hipStream_t st) {
     float* part = !a.d_bias ? nullptr : rows == 1 ? a.d_bias : (float*)(ws + l.part);
     e = a.cu ? launch_tiles<gated_bwd_kernel<T, V, S, true, CODES, NARROW>>(tl, st, a, tl, part)
              : launch_tiles<gated_bwd_kernel<T, V, S, false, CODES, NARROW>>(tl, st, a, tl, part);
-    if (e != hipSuccess || !a.d_bias || rows == 1) return e;
+    if (e != hipSuccess || !a.d_bias || rows == 1 || l.fused) return e;
     gated_dbias_kernel<<<(unsigned)((a.D + 31) / 32), kThreads, 0, st>>>(part, a.d_bias, rows,
                                                                          a.D);
     return hipGetLastError();

@@ -38,6 +38,8 @@ SHAPES = [  # B, T, D: one step, around a chunk's and a tile's borders, odd widt
     (1, 1, 1), (3, 1, 64), (2, 2, 7), (1, 63, 65), (2, 64, 64), (1, 65, 130), (5, 127, 33),
     (1, 128, 66), (2, 255, 100), (1, 256, 64), (1, 257, 192), (2, 513, 1001), (1, 1025, 20),
     (1, 2049, 256), (1, 5003, 48), (300, 3, 5),
+    # chains that the tile counters share out evenly, nearly, or not at all
+    (9, 50, 64), (7, 300, 64), (63, 20, 40), (3, 700, 576), (67, 260, 8), (1, 400, 3000),
 ]
 
 
@@ -95,6 +97,49 @@ def test_packed_row(T, D, nseq, dtype):
                                 cu_seqlens=d["cu"])
     assert out["d_init"] is None
     check_grads(out, want, c, half, T)
+
+
+@pytest.mark.parametrize("nseq", [0, 3])
+def test_long_row(nseq):
+    """So many tiles to a chain that the carry goes over all of its levels (tiles, 16 and 256
+    of them), with gates that remember hundreds of steps."""
+    T, D = 67000, 5
+    v = make(1, T, D, "fp32", seed=6, nseq=nseq, slow=3.5)
+    x, g, bias, cu, r = reference(v)
+    d = cuda(v)
+    saved = binding.ssd_gated_saved(halves(d["xg"])[0])
+    h, final = forward(d, saved)
+    c = c_of(g, bias)
+    check("h", h, r["h"], r["h_mag"], c)
+    check("final", final, r["final"], r["final_mag"], c)
+    check("entry", saved["entry_states"], r["entry"], r["entry_mag"], c)
+    want = gated.gated_bwd_ref(x, g, bias, n64(saved["entry_states"]), n64(v["dh"]),
+                               n64(v["d_final"]), cu)
+    xd, gd = halves(d["xg"])
+    out = binding.ssd_gated_bwd(xd, gd, d["bias"], d["dh"], saved, d_final=d["d_final"],
+                                cu_seqlens=d["cu"])
+    check_grads(out, want, c, 2.0 ** -24, T)
+
+
+def test_every_call_on_a_stream_of_its_own():
+    """The stream argument: outputs and workspaces made inside belong to that stream."""
+    v = make(2, 700, 130, "bf16", seed=13)
+    d = cuda(v)
+    xd, gd = halves(d["xg"])
+
+    def run(**kw):
+        saved = binding.ssd_gated_saved(xd, ckpt=True)
+        torch.cuda.synchronize()
+        h, final = forward(d, saved, **kw)
+        a = binding.ssd_gated_bwd(xd, gd, d["bias"], d["dh"], saved, d_final=d["d_final"], **kw)
+        b = binding.ssd_gated_bwd_ckpt(d["bias"], d["dh"], saved, d_final=d["d_final"], **kw)
+        y = binding.ssd_gated_step(xd[:, 0], gd[:, 0], d["bias"], final, **kw)
+        torch.cuda.synchronize()
+        return [h, final, y, *(o[k] for o in (a, b) for k in ("dx", "dg", "d_bias", "d_init"))]
+
+    want = run()
+    got = run(stream=torch.cuda.Stream())
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
 @pytest.mark.parametrize("cu", [[0, 64, 128, 192, 256, 320], [0, 0, 0, 256, 256, 512, 512],
