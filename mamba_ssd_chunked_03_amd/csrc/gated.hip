@@ -422,6 +422,36 @@ __device__ __forceinline__ void pack_run(const Piece<T, V> (&v)[S], int8_t* code
     }
 }
 
+// A kernel's one argument.  FRESH: read anew where it is asked for, from the start of the
+// segment that kernel arguments lie in.  Kept over a whole tile, its fields and what is made
+// of them take more scalar registers than there are, and those that do not fit cost vector
+// instructions and registers; read anew, the next access waits for a scalar load.
+// In us, kept and read anew:
+//   FRESH  forward with codes: the training pass from codes at 8 x 2048 x 1536 in bf16 118, 113;
+//          backward in bf16: 4 x 4096 x 5120 equal, a packed row of 16384 x 2048 102, 100
+//   not    forward without codes: 4 x 4096 x 5120 in bf16 99, 113; backward in fp32: a packed
+//          row of 5001 x 1280 40, 42
+template <bool FRESH, typename A> __device__ __forceinline__ A args(const A& in) {
+    if (!FRESH) return in;
+    static_assert(sizeof(A) % 8 == 0, "copied in words of 64 bits");
+    typedef const uint64_t __attribute__((address_space(4))) Word;
+    Word* p = (Word*)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    union { A a; uint64_t w[sizeof(A) / 8]; } u;
+#pragma unroll
+    for (unsigned i = 0; i < sizeof(A) / 8; ++i) u.w[i] = p[i];
+    return u.a;
+}
+struct FwdParams {
+    GatedFwdArgs a;
+    Tiles tl;
+};
+struct BwdParams {
+    GatedBwdArgs a;
+    Tiles tl;
+    float* part;  // d_bias' sums of the tiles, or null
+};
+
 // threadIdx.x, computed anew in every iteration: the addresses that follow from it would
 // otherwise be kept over the whole loop, in more registers than there are.
 __device__ __forceinline__ int fresh_thread() {
@@ -432,18 +462,27 @@ __device__ __forceinline__ int fresh_thread() {
 
 // ---- forward ------------------------------------------------------------------------------
 template <typename T, int V, int S, bool PACKED, bool CODES, bool NARROW>
-__global__ __launch_bounds__(kRuns * kLanes, 4) void gated_fwd_kernel(GatedFwdArgs a, Tiles tl) {
+__global__ __launch_bounds__(kRuns * kLanes, 4) void gated_fwd_kernel(FwdParams in) {
+    constexpr bool FRESH = CODES;
     constexpr int C = kLanes * V, kTile = kRuns * S;
     __shared__ __align__(16) float sP[kRuns * C], sH[kRuns * C], sE[C];
     __shared__ unsigned sFirst, sNext, sCut[kRuns];
-    const Group group = group_of(tl);
-    unsigned t = first_number(tl, group, &sFirst);
+    Group group;
+    unsigned t;
+    {
+        const Tiles tl = args<FRESH>(in).tl;
+        group = group_of(tl);
+        t = first_number(tl, group, &sFirst);
+    }
     if (t >= group.tiles) return;
     Place w;
     Piece<T, V> x[S], g[S];
     float bias[V];
     RunSeqs seqs;
     auto fetch = [&]() {
+        const FwdParams p = args<FRESH>(in);
+        const GatedFwdArgs& a = p.a;
+        const Tiles& tl = p.tl;
         w = place<V, NARROW>(tl, group, t, a.D);
         const int t0 = w.k * kTile, rows = min(kTile, a.T - t0);
         if (PACKED) seqs.load(tl, t0 + w.r * S);
@@ -457,6 +496,9 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_fwd_kernel(GatedFwdAr
     fetch();
     for (;;) {
         const int tid = fresh_thread();
+        const FwdParams p1 = args<FRESH>(in);
+        const GatedFwdArgs& a = p1.a;
+        const Tiles& tl = p1.tl;
         const int t0 = w.k * kTile, ts = t0 + w.r * S;
         const int rows = min(kTile, a.T - t0);
         const bool whole = rows == kTile;
@@ -532,6 +574,9 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_fwd_kernel(GatedFwdAr
                     accP *= p[r];
                 }
             }
+            const FwdParams p2 = args<FRESH>(in);
+            const GatedFwdArgs& a = p2.a;
+            const Tiles& tl = p2.tl;
             bool owned;
             const int c = channel_of<V, NARROW>(w.cb, col, a.D, &owned);
             const float first =
@@ -556,22 +601,23 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_fwd_kernel(GatedFwdAr
             for (int i = 0; i < V; ++i) h[i] = cut ? h[i] : fmaf(p[i], e[i], h[i]);
         }
         if (w.o.any()) {
+            const FwdParams p3 = args<FRESH>(in);
+            const GatedFwdArgs& a = p3.a;
             if (a.entry && ts % kGatedChunk == 0 && ts < a.T) {
                 const long long nC = (a.T + kGatedChunk - 1) / kGatedChunk;
                 store<float, V>(a.entry + (w.b * nC + ts / kGatedChunk) * a.D + w.o.c0, h, w.o);
             }
+            char* const out = (char*)((T*)a.h + row0 * a.D);
+            uint32_t off = row_offset<T>(w.r * S, a.D, w.o.c0);
 #pragma unroll
-            for (int j = 0; j < S; ++j) {
+            for (int j = 0; j < S; ++j, off += a.D * (uint32_t)sizeof(T)) {
                 if (PACKED && (starts >> j & 1)) {
 #pragma unroll
                     for (int i = 0; i < V; ++i) h[i] = 0.f;
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) h[i] = gate_step(q[j][i], x[j].get(i), h[i]);
-                if (whole || ts + j < a.T)
-                    store<T, V>((T*)((char*)((T*)a.h + (row0 + j) * a.D) +
-                                     row_offset<T>(w.r * S, a.D, w.o.c0)),
-                                h, w.o);
+                if (whole || ts + j < a.T) store<T, V>((T*)(out + off), h, w.o);
                 if (PACKED && a.final_state && (ends >> j & 1)) {
                     const long long seq = sequence_ending(a.cu, a.nseq, from, ts + j);
                     store<float, V>(a.final_state + seq * a.D + w.o.c0, h, w.o);
@@ -624,13 +670,16 @@ template <typename T, int V, int S, bool NARROW> struct RunIn<T, V, S, true, NAR
         scales += row0 * groups;
         const uint32_t group =
             min((w.cb * kLanes + w.cq) * V / SSD_CKPT_GROUP, groups - 1);
+        const uint32_t last = (uint32_t)(rows - 1) * (uint32_t)D + (uint32_t)w.o.c0;
+        const uint32_t slast = (uint32_t)(rows - 1) * (uint32_t)groups + group;
+        uint32_t at = (uint32_t)(w.r * S) * (uint32_t)D + (uint32_t)w.o.c0;
+        uint32_t sat = (uint32_t)(w.r * S) * (uint32_t)groups + group;
 #pragma unroll
-        for (int j = 0; j < S; ++j) {
-            const uint32_t row = min(w.r * S + j, rows - 1);
-            const int8_t* p = codes + (row * (uint32_t)D + (uint32_t)w.o.c0);
+        for (int j = 0; j < S; ++j, at += D, sat += groups) {
+            const int8_t* p = codes + min(at, last);
             if (NARROW) v[j].load_part(p, w.o.hi);
             else v[j].load(p);
-            s[j] = scales[row * (uint32_t)groups + group];
+            s[j] = scales[min(sat, slast)];
         }
     }
     __device__ __forceinline__ float get(int j, int i) const { return v[j].get(i) * s[j]; }
@@ -642,8 +691,8 @@ template <typename T, int V, int S, bool NARROW> struct RunIn<T, V, S, true, NAR
 };
 
 template <typename T, int V, int S, bool PACKED, bool CODES, bool NARROW>
-__global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdArgs a, Tiles tl,
-                                                                     float* part) {
+__global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(BwdParams in) {
+    constexpr bool FRESH = sizeof(T) == 2;
     constexpr int C = kLanes * V, kTile = kRuns * S;
     constexpr int kChunkRuns = kGatedChunk / S;
     static_assert(kTile % kGatedChunk == 0 && kRuns * kLanes >= 3 * C, "tiles hold whole chunks");
@@ -652,8 +701,15 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
     __shared__ __align__(16) float sE[C];
     __shared__ __align__(16) float sD[kWaves * C];  // d_bias' share of every wave
     __shared__ unsigned sFirst, sNext, sCut[kRuns];
-    const Group group = group_of(tl);
-    unsigned t = first_number(tl, group, &sFirst);
+    Group group;
+    unsigned t;
+    bool sums;  // d_bias is wanted
+    {
+        const BwdParams p = args<FRESH>(in);
+        sums = p.part != nullptr;
+        group = group_of(p.tl);
+        t = first_number(p.tl, group, &sFirst);
+    }
     if (t >= group.tiles) return;
     Place w;
     RunIn<T, V, S, CODES, NARROW> x, g;
@@ -661,6 +717,9 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
     float bias[V];
     RunSeqs seqs;
     auto fetch = [&]() {
+        const BwdParams p = args<FRESH>(in);
+        const GatedBwdArgs& a = p.a;
+        const Tiles& tl = p.tl;
         w = place<V, NARROW>(tl, group, t, a.D);
         const int t0 = (tl.nk - 1 - w.k) * kTile, rows = min(kTile, a.T - t0);  // last tile first
         if (PACKED) seqs.load(tl, t0 + w.r * S);
@@ -675,6 +734,10 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
     before.k = -1;
     // one wave; with tl.done the last tile of the channel block adds up all of them
     auto sum_up = [&](int col) {
+        const BwdParams p = args<FRESH>(in);
+        const GatedBwdArgs& a = p.a;
+        const Tiles& tl = p.tl;
+        float* const part = p.part;
         bool owned;
         const int c = channel_of<V, NARROW>(before.cb, col, a.D, &owned);
         float s = 0.f;
@@ -717,6 +780,9 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
     fetch();
     for (;;) {
         const int tid = fresh_thread();
+        const BwdParams p1 = args<FRESH>(in);
+        const GatedBwdArgs& a = p1.a;
+        const Tiles& tl = p1.tl;
         const int kt = tl.nk - 1 - w.k;
         const int t0 = kt * kTile, ts = t0 + w.r * S;
         const int rows = min(kTile, a.T - t0);
@@ -742,6 +808,8 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
         }
         // d_final of a packed sequence that ends at step j of this run
         auto ending = [&](int j, float (&v)[V]) {
+            const BwdParams p = args<FRESH>(in);
+            const GatedBwdArgs& a = p.a;
             const float* d = nullptr;
             if (a.d_final) {
                 const long long seq = sequence_ending(a.cu, a.nseq, from, ts + j);
@@ -751,17 +819,20 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
         };
         {
             // G's carry out of the run in the same sweep: dh_j reaches it through the product
-            // of a up to j
-            float P[V], H[V], G[V];
+            // of a up to j; behind the run's first start nothing does
+            float P[V], H[V], G[V], kept[V];
             bool cut = false;
 #pragma unroll
             for (int i = 0; i < V; ++i) P[i] = 1.f, H[i] = G[i] = 0.f;
 #pragma unroll
             for (int j = 0; j < S; ++j) {
                 if (PACKED && (starts >> j & 1)) {
-                    cut = true;
 #pragma unroll
-                    for (int i = 0; i < V; ++i) H[i] = 0.f;
+                    for (int i = 0; i < V; ++i) {
+                        kept[i] = cut ? kept[i] : G[i];
+                        H[i] = 0.f;
+                    }
+                    cut = true;
                 }
 #pragma unroll
                 for (int i = 0; i < V; ++i) {
@@ -769,7 +840,7 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
                     if (!whole && ts + j >= a.T) q = 0.f;
                     H[i] = gate_step(q, x.get(j, i), H[i]);
                     P[i] = fmaf(-q, P[i], P[i]);
-                    if (!cut) G[i] = fmaf(P[i], dh[j].get(i), G[i]);
+                    G[i] = fmaf(P[i], dh[j].get(i), G[i]);
                 }
                 if (PACKED && !cut && (ends >> j & 1)) {
                     float v[V];
@@ -777,6 +848,10 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
 #pragma unroll
                     for (int i = 0; i < V; ++i) G[i] = fmaf(P[i], v[i], G[i]);
                 }
+            }
+            if (PACKED && cut) {
+#pragma unroll
+                for (int i = 0; i < V; ++i) G[i] = kept[i];
             }
             put<V>(&sP[w.r * C], w.cq, P);
             put<V>(&sH[w.r * C], w.cq, H);
@@ -808,6 +883,9 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
                     accP *= p[r];
                 }
             }
+            const BwdParams p2 = args<FRESH>(in);
+            const GatedBwdArgs& a = p2.a;
+            const Tiles& tl = p2.tl;
             bool owned;
             const int c = channel_of<V, NARROW>(w.cb, col, a.D, &owned);
             const float first =
@@ -817,6 +895,8 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
             sE[col] = carry_in<C>(tl, w.tile, w.k, col, cuts ? kCut : accP, accC, first);
         } else if (tid < 2 * C) {  // the next: h, from every chunk's entry state
             const int col = tid - C;
+            const BwdParams p2 = args<FRESH>(in);
+            const GatedBwdArgs& a = p2.a;
             bool owned;
             const int c = channel_of<V, NARROW>(w.cb, col, a.D, &owned);
             const int nC = (a.T + kGatedChunk - 1) / kGatedChunk;
@@ -838,7 +918,7 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
                 }
             }
         } else if (tid < 3 * C) {
-            if (part && before.k >= 0) sum_up(tid - 2 * C);
+            if (sums && before.k >= 0) sum_up(tid - 2 * C);
         }
         __syncthreads();
         float h[V], G[V], db[V];
@@ -876,8 +956,15 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
             }
         }
         g.again();
+        const BwdParams p3 = args<FRESH>(in);
+        const uint32_t dx_step = (uint32_t)p3.a.dx_stride * (uint32_t)sizeof(T);
+        const uint32_t dg_step = (uint32_t)p3.a.dg_stride * (uint32_t)sizeof(T);
+        char* const to_dx = (char*)((T*)p3.a.dx + row0 * p3.a.dx_stride);
+        char* const to_dg = (char*)((T*)p3.a.dg + row0 * p3.a.dg_stride);
+        uint32_t dx_off = row_offset<T>(w.r * S + S - 1, p3.a.dx_stride, w.o.c0);
+        uint32_t dg_off = row_offset<T>(w.r * S + S - 1, p3.a.dg_stride, w.o.c0);
 #pragma unroll
-        for (int j = S - 1; j >= 0; --j) {
+        for (int j = S - 1; j >= 0; --j, dx_off -= dx_step, dg_off -= dg_step) {
             if (PACKED && (ends >> j & 1)) ending(j, G);
             if (whole || ts + j < a.T) {
                 float dx[V], dg[V];
@@ -888,19 +975,19 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
                     dx[i] = e.q * v;
                     dg[i] = dx[i] * e.a * off[j][i];
                     db[i] += dg[i];
-                    G[i] = PACKED && (starts >> j & 1) ? 0.f : fmaf(-e.q, v, v);
+                    G[i] = fmaf(-e.q, v, v);
                 }
-                store<T, V>((T*)((char*)((T*)a.dx + (row0 + j) * a.dx_stride) +
-                                 row_offset<T>(w.r * S, a.dx_stride, w.o.c0)),
-                            dx, w.o);
-                store<T, V>((T*)((char*)((T*)a.dg + (row0 + j) * a.dg_stride) +
-                                 row_offset<T>(w.r * S, a.dg_stride, w.o.c0)),
-                            dg, w.o);
+                store<T, V>((T*)(to_dx + dx_off), dx, w.o);
+                store<T, V>((T*)(to_dg + dg_off), dg, w.o);
+                if (PACKED && (starts >> j & 1)) {
+#pragma unroll
+                    for (int i = 0; i < V; ++i) G[i] = 0.f;
+                }
             }
         }
-        if (!PACKED && a.d_init && ts == 0)
-            store<float, V>(a.d_init + (long long)w.b * a.D + w.o.c0, G, w.o);
-        if (part) {  // the wave's four runs; summed up during the next tile's scan
+        if (!PACKED && p3.a.d_init && ts == 0)
+            store<float, V>(p3.a.d_init + (long long)w.b * p3.a.D + w.o.c0, G, w.o);
+        if (sums) {  // the wave's four runs; summed up during the next tile's scan
 #pragma unroll
             for (int i = 0; i < V; ++i) db[i] = row_sum(db[i]);
             if (tid % 64 < kLanes) put<V>(&sD[tid / 64 * C], w.cq, db);
@@ -911,7 +998,7 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(GatedBwdAr
         fetch();
         __syncthreads();  // LDS is free again
     }
-    if (part) {
+    if (sums) {
         __syncthreads();
         if (threadIdx.x < C) sum_up(threadIdx.x);
     }
@@ -971,8 +1058,8 @@ __global__ __launch_bounds__(kThreads) void gated_prep_kernel(Prep p) {
     }
 }
 
-// d_bias from the tiles' sums, where there are many: a workgroup per 32 channels, 8 threads per channel; fixed
-// order.
+// d_bias from the tiles' sums, where there are many: a workgroup per 32 channels, 8 threads
+// per channel; fixed order.
 __global__ __launch_bounds__(kThreads) void gated_dbias_kernel(const float* part, float* d_bias,
                                                                int rows, int D) {
     __shared__ float s[8][32];
@@ -1126,8 +1213,9 @@ size_t gated_workspace_bytes(int B, int T, int D) {
 
 namespace {
 // As many workgroups as are resident at once, and no more per counter than its tiles.
-template <auto kern, typename... Args>
-hipError_t launch_tiles(const Tiles& tl, hipStream_t st, Args... args) {
+template <auto kern, typename Params>
+hipError_t launch_tiles(const Params& p, hipStream_t st) {
+    const Tiles& tl = p.tl;
     static DeviceSlots slots;
     int grid = 0;
     const hipError_t e =
@@ -1137,7 +1225,7 @@ hipError_t launch_tiles(const Tiles& tl, hipStream_t st, Args... args) {
         ((long long)tl.chains + tl.groups - 1) / tl.groups * tl.nk * tl.groups;
     if (grid > most) grid = (int)most;
     grid -= grid % tl.groups;
-    kern<<<grid, kRuns * kLanes, 0, st>>>(args...);
+    kern<<<grid, kRuns * kLanes, 0, st>>>(p);
     return hipGetLastError();
 }
 
@@ -1148,8 +1236,9 @@ hipError_t run_fwd(const GatedFwdArgs& a, char* ws, hipStream_t st) {
     const hipError_t e = prepare(l, ws, a.cu, a.nseq, a.T, a.D, a.final_state, st);
     if (e != hipSuccess) return e;
     const Tiles tl = tiles_of(l, a.B, kLanes * V, ws, a.cu != nullptr);
-    return a.cu ? launch_tiles<gated_fwd_kernel<T, V, S, true, CODES, NARROW>>(tl, st, a, tl)
-                : launch_tiles<gated_fwd_kernel<T, V, S, false, CODES, NARROW>>(tl, st, a, tl);
+    const FwdParams p{a, tl};
+    return a.cu ? launch_tiles<gated_fwd_kernel<T, V, S, true, CODES, NARROW>>(p, st)
+                : launch_tiles<gated_fwd_kernel<T, V, S, false, CODES, NARROW>>(p, st);
 }
 
 template <typename T, ssd_dtype DT, bool CODES, bool NARROW>
@@ -1161,8 +1250,9 @@ hipError_t run_bwd(const GatedBwdArgs& a, char* ws, hipStream_t st) {
     const Tiles tl = tiles_of(l, a.B, kLanes * V, ws, a.cu != nullptr);
     const int rows = a.B * l.nk;
     float* part = !a.d_bias ? nullptr : rows == 1 ? a.d_bias : (float*)(ws + l.part);
-    e = a.cu ? launch_tiles<gated_bwd_kernel<T, V, S, true, CODES, NARROW>>(tl, st, a, tl, part)
-             : launch_tiles<gated_bwd_kernel<T, V, S, false, CODES, NARROW>>(tl, st, a, tl, part);
+    const BwdParams p{a, tl, part};
+    e = a.cu ? launch_tiles<gated_bwd_kernel<T, V, S, true, CODES, NARROW>>(p, st)
+             : launch_tiles<gated_bwd_kernel<T, V, S, false, CODES, NARROW>>(p, st);
     if (e != hipSuccess || !a.d_bias || rows == 1 || l.fused) return e;
     gated_dbias_kernel<<<(unsigned)((a.D + 31) / 32), kThreads, 0, st>>>(part, a.d_bias, rows,
                                                                          a.D);
