@@ -1011,6 +1011,7 @@ constexpr int kPrepSeqs = 2048;
 
 // Before a pass: the counters cleared, spans and carries marked missing, the start bits of a
 // packed row, and zero final states for its empty sequences.
+// Cached stores: non-temporal ones took 1 us longer (4 x 4096 x 5120, 2.8 MB).
 struct Prep {
     unsigned* clear;       // counters, then spans and carries: words to set
     long long zeros, words;  // the first to 0, the others to kNotYet
@@ -1026,9 +1027,8 @@ __global__ __launch_bounds__(kThreads) void gated_prep_kernel(Prep p) {
     const long long id = (long long)blockIdx.x * kThreads + threadIdx.x;
     const long long all = (long long)gridDim.x * kThreads;
     for (long long i = id; i < p.words / 4; i += all)
-        __builtin_nontemporal_store(i < p.zeros / 4 ? Words<4>{0, 0, 0, 0}
-                                                    : Words<4>{~0u, ~0u, ~0u, ~0u},
-                                    reinterpret_cast<Words<4>*>(p.clear) + i);
+        reinterpret_cast<Words<4>*>(p.clear)[i] =
+            i < p.zeros / 4 ? Words<4>{0, 0, 0, 0} : Words<4>{~0u, ~0u, ~0u, ~0u};
     if (!p.starts) return;
     auto mark = [&](const int* cu) {
         for (long long i = id; i < p.bytes; i += all) {
