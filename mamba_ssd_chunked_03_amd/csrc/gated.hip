@@ -18,8 +18,8 @@
 // first, for G.
 //
 // Bound by HBM: 3 (forward) or 5 (backward) values per element in and out.  At 4 x 4096 x 5120
-// in bf16 the forward takes 100 us (503 MB, 5.0 TB/s: what a large copy reaches here) and the
-// backward 182 us (839 MB, 4.6 TB/s); a forward in three kernels would read x and g twice, 5
+// in bf16 the forward takes 99 us (503 MB, 5.1 TB/s: what a large copy reaches here) and the
+// backward 182 us (844 MB, 4.6 TB/s); a forward in three kernels would read x and g twice, 5
 // values per element.  One tile alone takes 5.5 us from launch to end; what lies between
 // that and HBM's time at medium sizes is the wait for the carry and the prep launch (2 us).
 //
@@ -44,10 +44,10 @@ constexpr int kScan = 8;    // runs that a scan reads together
 // V channels by S steps of a lane.  16 or 32 elements a lane in 16 or 8 byte pieces were
 // measured, at 4 x 4096 x 5120 (backward, and forward with codes at 8 x 2048 x 1536), at one
 // row of 65536 x 5120 (forward) and of 65536 x 256 (thin):
-//   bf16 forward  4 x 8: 100, 399, thin 37 us;    8 x 4: 100, 411, 40;   4 x 4: 105, 461, 51
-//   with codes    8 x 4: 118 us for the training pass;  4 x 8: 127: the 8-bit scales' two
+//   bf16 forward  4 x 8: 99, 393, thin 31 us;    8 x 4: 100, 414, 36;   4 x 4: 122, 531, 43
+//   with codes    8 x 4: 114 us for the training pass;  4 x 8: 124: the 8-bit scales' two
 //                 divisions come once per step and lane
-//   bf16 backward 4 x 8: 183 us;  4 x 4: 189;  8 x 4: 228 (more registers than there are)
+//   bf16 backward 4 x 8: 183 us;  4 x 4: 200;  8 x 4: 228 (more registers than there are)
 //   fp32          4 x 8 forward, 4 x 4 backward: the same bytes a lane as in bf16
 constexpr int fwd_vec(ssd_dtype t, bool codes) { return t == SSD_BF16 && codes ? 8 : 4; }
 constexpr int fwd_steps(ssd_dtype t, bool codes) { return t == SSD_BF16 && codes ? 4 : 8; }
