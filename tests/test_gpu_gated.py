@@ -495,6 +495,35 @@ def test_more_than_2_to_32_elements():
         assert float((a - b)[:, :440].abs().max()) <= 64 * 2 ** -8 + s
 
 
+@pytest.mark.parametrize("B,T,stride", [(3, 1, 2 ** 29 + 8), (2, 4, 2 ** 27 - 1)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_rows_far_apart(B, T, stride, dtype):
+    """Rows as far apart as their offsets inside a tile allow, inputs and gradients: the bits of
+    contiguous rows, and 8-bit checkpoints of them the same."""
+    D = 9
+    v = make(B, T, D, dtype, seed=T)
+    d = cuda(v)
+    xc, gc = (t.contiguous() for t in halves(d["xg"]))
+    rows = torch.empty((B * T - 1) * stride + 5 * D, dtype=DTYPES[dtype], device="cuda")
+    x, g, dh, dx, dg = (rows.as_strided((B, T, D), (T * stride, stride, 1), i * D)
+                        for i in range(5))
+    for to, of in ((x, xc), (g, gc), (dh, d["dh"])):
+        to.copy_(of)
+    got, want = [], []
+    for xs, gs, dhs, out, res in ((x, g, dh, dict(dx=dx, dg=dg), got),
+                                  (xc, gc, d["dh"], None, want)):
+        saved = binding.ssd_gated_saved(xc, ckpt=True)
+        res += binding.ssd_gated_fwd(xs, gs, d["bias"], init_state=d["init"], saved=saved)
+        res += saved.values()
+        o = binding.ssd_gated_bwd(xs, gs, d["bias"], dhs, saved, d_final=d["d_final"], out=out)
+        res += [o[k] for k in ("dx", "dg", "d_bias", "d_init")]
+        o = binding.ssd_gated_bwd_ckpt(d["bias"], dhs, saved, d_final=d["d_final"])
+        res += [o[k] for k in ("dx", "dg", "d_bias", "d_init")]
+        state = d["init"].clone()
+        res += [binding.ssd_gated_step(xs[:, 0], gs[:, 0], d["bias"], state), state]
+    assert len(got) == len(want) and all(torch.equal(p, q) for p, q in zip(got, want))
+
+
 def test_calls_on_the_layer_s_own_tensors():
     """The recurrence next to the layer: the block's prologue makes x and the gate's rows come
     from the same projection; the epilogue takes its output."""
