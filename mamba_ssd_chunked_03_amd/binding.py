@@ -810,7 +810,7 @@ def _launch(fn, dev, *args):
     index = dev.index
     if dev.type != "cuda" or index is None:
         raise ValueError(f"tensors must be on a GPU, got {dev}")
-    if index == torch.cuda.current_device():
+    if index == _device_index():
         code = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(dev):
@@ -823,6 +823,8 @@ def _launch(fn, dev, *args):
 # first, which takes 2 us of the 6 that a small call spends in this module
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda index: torch.cuda.current_stream(index).cuda_stream)
+# the current device, without asking again whether the GPU is initialised
+_device_index = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _addr(t):
