@@ -57,8 +57,9 @@ constexpr int bwd_steps(ssd_dtype t) { return t == SSD_BF16 ? 8 : 4; }
 // ---- pieces: a lane's V neighbouring channels of a row -------------------------------------
 // Rows need only element alignment, so pieces are loaded and stored as unaligned vectors (one
 // access each; the hardware takes any alignment).
-// Non-temporal, since every row is read and written once: at 4 x 4096 x 5120 in bf16 the
-// forward takes 98 us so and 110 us with cached accesses, the backward 188 and 219.
+// Stores of rows are non-temporal, since every row is written once: at 4 x 4096 x 5120 in bf16
+// the forward takes 99 us so and 101 us with cached stores, the backward 184 and 193.  Loads of
+// rows are non-temporal where the call's rows are large (kCachedBytes).
 template <int WORDS> using Words = uint32_t __attribute__((ext_vector_type(WORDS)));
 template <typename T, int WORDS> struct AnyWords {
     typedef Words<WORDS> Any __attribute__((aligned(sizeof(T))));
@@ -375,7 +376,7 @@ __device__ __forceinline__ uint32_t row_offset(int row, long long stride, int c0
 // Load a run's pieces: step ts + j is the tile's row `run * S + j`; base: the tile's first
 // row; rows: the tile's rows that exist (steps behind repeat the last one; the caller clears
 // them).  No branch: one would make the loads of x wait for those of g.
-template <typename T, int V, int S, bool NARROW>
+template <typename T, int V, int S, bool NARROW, bool CACHED>
 __device__ __forceinline__ void load_run(Piece<T, V> (&q)[S], const void* base, long long stride,
                                          int run, int rows, const Own& o) {
     const uint32_t last = row_offset<T>(rows - 1, stride, o.c0);
@@ -385,6 +386,7 @@ __device__ __forceinline__ void load_run(Piece<T, V> (&q)[S], const void* base, 
     for (int j = 0; j < S; ++j, off += step) {
         const T* p = (const T*)((const char*)base + min(off, last));
         if (NARROW) q[j].load_part(p, o.hi);
+        else if (CACHED) q[j].load_cached(p);
         else q[j].load(p);
     }
 }
@@ -461,7 +463,7 @@ __device__ __forceinline__ int fresh_thread() {
 }
 
 // ---- forward ------------------------------------------------------------------------------
-template <typename T, int V, int S, bool PACKED, bool CODES, bool NARROW>
+template <typename T, int V, int S, bool PACKED, bool CODES, bool NARROW, bool CACHED>
 __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_fwd_kernel(FwdParams in) {
     constexpr bool FRESH = CODES;
     constexpr int C = kLanes * V, kTile = kRuns * S;
@@ -488,10 +490,10 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_fwd_kernel(FwdParams 
         if (PACKED) seqs.load(tl, t0 + w.r * S);
         const long long row0 = (long long)w.b * a.T + t0;
         load_f32<V, NARROW>(bias, a.bias ? a.bias + w.o.c0 : nullptr, w.o);
-        load_run<T, V, S, NARROW>(g, (const T*)a.g + row0 * a.g_stride, a.g_stride, w.r, rows,
-                                  w.o);
-        load_run<T, V, S, NARROW>(x, (const T*)a.x + row0 * a.x_stride, a.x_stride, w.r, rows,
-                                  w.o);
+        load_run<T, V, S, NARROW, CACHED>(g, (const T*)a.g + row0 * a.g_stride, a.g_stride,
+                                          w.r, rows, w.o);
+        load_run<T, V, S, NARROW, CACHED>(x, (const T*)a.x + row0 * a.x_stride, a.x_stride,
+                                          w.r, rows, w.o);
     };
     fetch();
     for (;;) {
@@ -644,13 +646,15 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // x and g of a run, from rows in T or from 8-bit codes and their scales.
-template <typename T, int V, int S, bool CODES, bool NARROW> struct RunIn;
-template <typename T, int V, int S, bool NARROW> struct RunIn<T, V, S, false, NARROW> {
+template <typename T, int V, int S, bool CODES, bool NARROW, bool CACHED> struct RunIn;
+template <typename T, int V, int S, bool NARROW, bool CACHED>
+struct RunIn<T, V, S, false, NARROW, CACHED> {
     Piece<T, V> v[S];
     __device__ __forceinline__ void load(const void* from, long long stride, const int8_t*,
                                          const float*, long long row0, int rows, const Place& w,
                                          int) {
-        load_run<T, V, S, NARROW>(v, (const T*)from + row0 * stride, stride, w.r, rows, w.o);
+        load_run<T, V, S, NARROW, CACHED>(v, (const T*)from + row0 * stride, stride, w.r, rows,
+                                          w.o);
     }
     __device__ __forceinline__ float get(int j, int i) const { return v[j].get(i); }
     __device__ __forceinline__ void clear(int j) { v[j].clear(); }
@@ -659,7 +663,8 @@ template <typename T, int V, int S, bool NARROW> struct RunIn<T, V, S, false, NA
         for (int j = 0; j < S; ++j) v[j].renew();
     }
 };
-template <typename T, int V, int S, bool NARROW> struct RunIn<T, V, S, true, NARROW> {
+template <typename T, int V, int S, bool NARROW, bool CACHED>
+struct RunIn<T, V, S, true, NARROW, CACHED> {
     CkptPiece<V> v[S];
     float s[S];
     __device__ __forceinline__ void load(const void*, long long, const int8_t* codes,
@@ -690,7 +695,7 @@ template <typename T, int V, int S, bool NARROW> struct RunIn<T, V, S, true, NAR
     }
 };
 
-template <typename T, int V, int S, bool PACKED, bool CODES, bool NARROW>
+template <typename T, int V, int S, bool PACKED, bool CODES, bool NARROW, bool CACHED>
 __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(BwdParams in) {
     constexpr bool FRESH = sizeof(T) == 2;
     constexpr int C = kLanes * V, kTile = kRuns * S;
@@ -712,7 +717,7 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(BwdParams 
     }
     if (t >= group.tiles) return;
     Place w;
-    RunIn<T, V, S, CODES, NARROW> x, g;
+    RunIn<T, V, S, CODES, NARROW, CACHED> x, g;
     Piece<T, V> dh[S];
     float bias[V];
     RunSeqs seqs;
@@ -727,8 +732,8 @@ __global__ __launch_bounds__(kRuns * kLanes, 4) void gated_bwd_kernel(BwdParams 
         load_f32<V, NARROW>(bias, a.bias ? a.bias + w.o.c0 : nullptr, w.o);
         g.load(a.g, a.g_stride, a.g_codes, a.g_scales, row0, rows, w, a.D);
         x.load(a.x, a.x_stride, a.x_codes, a.x_scales, row0, rows, w, a.D);
-        load_run<T, V, S, NARROW>(dh, (const T*)a.dh + row0 * a.dh_stride, a.dh_stride, w.r, rows,
-                                  w.o);
+        load_run<T, V, S, NARROW, CACHED>(dh, (const T*)a.dh + row0 * a.dh_stride, a.dh_stride,
+                                          w.r, rows, w.o);
     };
     Place before;  // the tile whose shares of d_bias are in sD
     before.k = -1;
@@ -1229,6 +1234,17 @@ hipError_t launch_tiles(const Params& p, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Cached loads where all rows of the call (`tensors` of them) take at most half of the 256 MB
+// cache between the L2s and HBM: its inputs were often made just before, and are there still.
+// In bf16, cached and non-temporal: 8 x 1024 x 1536 (75 MB) forward 17.3 and 21.2 us, (126 MB)
+// backward 32.4 and 36.7; 16384 x 2048 (336 MB) packed backward 103 and 101; 4 x 4096 x 5120
+// (503, 839 MB) forward 101.6 and 99.4, backward 194 and 184.
+constexpr long long kCachedBytes = 128ll << 20;
+template <typename T, bool NARROW>
+bool cached_rows(long long B, long long T_, long long D, int tensors) {
+    return !NARROW && B * T_ * D <= kCachedBytes / (long long)sizeof(T) / tensors;
+}
+
 template <typename T, ssd_dtype DT, bool CODES, bool NARROW>
 hipError_t run_fwd(const GatedFwdArgs& a, char* ws, hipStream_t st) {
     constexpr int V = fwd_vec(DT, CODES), S = fwd_steps(DT, CODES);
@@ -1237,8 +1253,12 @@ hipError_t run_fwd(const GatedFwdArgs& a, char* ws, hipStream_t st) {
     if (e != hipSuccess) return e;
     const Tiles tl = tiles_of(l, a.B, kLanes * V, ws, a.cu != nullptr);
     const FwdParams p{a, tl};
-    return a.cu ? launch_tiles<gated_fwd_kernel<T, V, S, true, CODES, NARROW>>(p, st)
-                : launch_tiles<gated_fwd_kernel<T, V, S, false, CODES, NARROW>>(p, st);
+    const bool cached = cached_rows<T, NARROW>(a.B, a.T, a.D, 3);
+#define SSD_GATED_FWD(PACKED, CACHED) \
+    launch_tiles<gated_fwd_kernel<T, V, S, PACKED, CODES, NARROW, CACHED && !NARROW>>(p, st)
+    if (a.cu) return cached ? SSD_GATED_FWD(true, true) : SSD_GATED_FWD(true, false);
+    return cached ? SSD_GATED_FWD(false, true) : SSD_GATED_FWD(false, false);
+#undef SSD_GATED_FWD
 }
 
 template <typename T, ssd_dtype DT, bool CODES, bool NARROW>
@@ -1251,8 +1271,12 @@ hipError_t run_bwd(const GatedBwdArgs& a, char* ws, hipStream_t st) {
     const int rows = a.B * l.nk;
     float* part = !a.d_bias ? nullptr : rows == 1 ? a.d_bias : (float*)(ws + l.part);
     const BwdParams p{a, tl, part};
-    e = a.cu ? launch_tiles<gated_bwd_kernel<T, V, S, true, CODES, NARROW>>(p, st)
-             : launch_tiles<gated_bwd_kernel<T, V, S, false, CODES, NARROW>>(p, st);
+    const bool cached = cached_rows<T, NARROW>(a.B, a.T, a.D, CODES ? 3 : 5);
+#define SSD_GATED_BWD(PACKED, CACHED) \
+    launch_tiles<gated_bwd_kernel<T, V, S, PACKED, CODES, NARROW, CACHED && !NARROW>>(p, st)
+    if (a.cu) e = cached ? SSD_GATED_BWD(true, true) : SSD_GATED_BWD(true, false);
+    else e = cached ? SSD_GATED_BWD(false, true) : SSD_GATED_BWD(false, false);
+#undef SSD_GATED_BWD
     if (e != hipSuccess || !a.d_bias || rows == 1 || l.fused) return e;
     gated_dbias_kernel<<<(unsigned)((a.D + 31) / 32), kThreads, 0, st>>>(part, a.d_bias, rows,
                                                                          a.D);

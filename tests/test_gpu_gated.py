@@ -495,6 +495,36 @@ def test_more_than_2_to_32_elements():
         assert float((a - b)[:, :440].abs().max()) <= 64 * 2 ** -8 + s
 
 
+@pytest.mark.parametrize("nseq", [0, 9])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_small_and_large_calls_agree(dtype, nseq):
+    """Rows are loaded in another way where a call has many: the same bits as for a part of its
+    channels alone."""
+    T, D, n = 4096, 12288 if dtype == "bf16" else 6144, 192  # 300 MB of rows or more
+    v = cuda(make(1, T, D, dtype, seed=2, nseq=nseq))
+    x, g = halves(v["xg"])
+    part = slice(128, 128 + n)
+
+    def run(x, g, bias, init, dh, d_final):
+        saved = binding.ssd_gated_saved(x, ckpt=True)
+        kw = dict(cu_seqlens=v["cu"])
+        res = [*binding.ssd_gated_fwd(x, g, bias, init_state=init, saved=saved, **kw)]
+        bare = binding.ssd_gated_saved(x)
+        res += [*binding.ssd_gated_fwd(x, g, bias, init_state=init, saved=bare, **kw)]
+        for o in (binding.ssd_gated_bwd(x, g, bias, dh, saved, d_final=d_final, **kw),
+                  binding.ssd_gated_bwd_ckpt(bias, dh, saved, d_final=d_final, **kw)):
+            res += [o[k] for k in ("dx", "dg", "d_bias", "d_init") if o[k] is not None]
+        return res + [saved["entry_states"], bare["entry_states"], saved["x_codes"],
+                      saved["g_codes"]]
+
+    full = (x, g, v["bias"], v["init"], v["dh"], v["d_final"])
+    cols = [None if t is None else t[..., part] for t in full]
+    cols[2:4] = [None if t is None else t.contiguous() for t in cols[2:4]]
+    cols[5] = cols[5].contiguous()
+    for a, b in zip(run(*full), run(*cols)):
+        assert torch.equal(a[..., part], b)
+
+
 @pytest.mark.parametrize("B,T,stride", [(3, 1, 2 ** 29 + 8), (2, 4, 2 ** 27 - 1)])
 @pytest.mark.parametrize("dtype", ["fp32", "bf16"])
 def test_rows_far_apart(B, T, stride, dtype):
