@@ -43,7 +43,7 @@ constexpr int kScan = 8;    // runs that a scan reads together
 
 // V channels by S steps of a lane.  16 or 32 elements a lane in 16 or 8 byte pieces were
 // measured, at 4 x 4096 x 5120 (backward, and forward with codes at 8 x 2048 x 1536), at one
-// row of 65536 x 5120 (forward) and of 65536 x 256 (thin):
+// row of 65536 x 5120 (forward) and of 65536 x 256 (thin; non-temporal loads):
 //   bf16 forward  4 x 8: 99, 393, thin 31 us;    8 x 4: 100, 414, 36;   4 x 4: 122, 531, 43
 //   with codes    8 x 4: 114 us for the training pass;  4 x 8: 124: the 8-bit scales' two
 //                 divisions come once per step and lane
@@ -183,8 +183,8 @@ __device__ __forceinline__ int channel_of(int cb, int col, int D, bool* owned) {
 constexpr int kBlockTiles = 16;  // tiles of a block of a chain, and blocks of a larger one
 // Counters of tiles taken, each for a range of neighbouring chains and on a cache line of its
 // own.  A counter serves one workgroup in about 9 ns: with one for all, the 512 workgroups
-// that start together wait 5 us for their first number (8 x 1024 x 1536 in bf16: forward 29
-// us, 22 with eight counters; backward 48 and 35).
+// that start together wait 5 us for their first number (8 x 1024 x 1536 in bf16: forward 24
+// us, 17 with eight counters; backward 42 and 32).
 constexpr unsigned kCounters = 8, kCounterWords = 64;
 
 struct Tiles {
@@ -1132,8 +1132,8 @@ struct Layout {
 };
 constexpr size_t kCounterBytes = kCounters * kCounterWords * 4;
 // d_bias from its tiles' sums: with so many tiles to a channel block or fewer the last one adds
-// them up (2 x 1003 x 1001 in fp32, 16 tiles: 17.7 us, 20.0 with a kernel of its own), behind
-// that a kernel of its own does (4 x 4096 x 5120, 64 tiles: 189 and 183; 32 tiles: equal).
+// them up (2 x 1003 x 1001 in fp32, 16 tiles: 17.0 us, 19.1 with a kernel of its own), behind
+// that a kernel of its own does (4 x 4096 x 5120, 64 tiles: 188 and 183; 32 tiles: equal).
 constexpr long long kFusedTiles = 16;
 size_t up256(size_t v) { return (v + 255) / 256 * 256; }
 // tiles of `steps` steps and `cols` channels
